@@ -206,3 +206,145 @@ extern "C" int gpt2k_embedding_bwd(const int32_t* idx, const float* dx, int B, i
     if (err != cudaSuccess) return set_error(GPT2_ERR_CUDA, cudaGetErrorString(err));
     return GPT2_OK;
 }
+
+// ---------------------------------------------------------------- 8-bit linear layers
+namespace {
+bool misaligned(const void* p, size_t bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
+size_t elem_size(int dtype) { return dtype == GPT2K_F32 ? 4 : 2; }
+}  // namespace
+
+extern "C" int gpt2k_quantize_rows(int dtype, const void* x, int rows, int K, int64_t ldx, int8_t* q, int64_t ldq,
+                                   float* scale, void* stream) {
+    if (dtype != GPT2K_F32 && dtype != GPT2K_BF16) return set_error(GPT2_ERR_INVALID_ARG, "unknown dtype");
+    if (rows < 1 || K < 1 || ldx < K || ldq < K)
+        return set_error(GPT2_ERR_INVALID_ARG, "need rows, K >= 1 and row strides >= K");
+    if (!x || !q || !scale) return set_error(GPT2_ERR_INVALID_ARG, "NULL operand");
+    if (misaligned(x, elem_size(dtype)) || misaligned(scale, 4))
+        return set_error(GPT2_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
+    long long launches = 0;
+    Ctx c = kctx(stream, nullptr, &launches);
+    if (dtype == GPT2K_F32)
+        launch_quantize_rows<float>(c, (const float*)x, ldx, rows, K, q, ldq, scale);
+    else
+        launch_quantize_rows<bf16>(c, (const bf16*)x, ldx, rows, K, q, ldq, scale);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return set_error(GPT2_ERR_CUDA, cudaGetErrorString(err));
+    return GPT2_OK;
+}
+
+extern "C" int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B, int64_t ldb,
+                               const float* b_scale, int M, int N, int K, int epilogue, int out_dtype, void* out,
+                               int64_t ldo, const float* bias, const float* resid, int64_t ldr, uint32_t* status_dev,
+                               void* stream) {
+    if (epilogue < GPT2K_EPI_STORE || epilogue > GPT2K_EPI_BIAS_RESID)
+        return set_error(GPT2_ERR_INVALID_ARG, "the int8 product has the epilogues store, bias, bias_gelu, bias_resid");
+    if (out_dtype != GPT2K_F32 && out_dtype != GPT2K_BF16) return set_error(GPT2_ERR_INVALID_ARG, "unknown dtype");
+    if (M < 1 || N < 1 || K < 1 || lda < K || ldb < K || ldo < N)
+        return set_error(GPT2_ERR_INVALID_ARG, "need M, N, K >= 1, lda, ldb >= K and ldo >= N");
+    if (K > I8_MAX_K) return set_error(GPT2_ERR_INVALID_ARG, "K above 131071: a 32-bit sum could overflow");
+    if (!A || !a_scale || !B || !b_scale || !out || !status_dev) return set_error(GPT2_ERR_INVALID_ARG, "NULL operand");
+    if (epilogue != GPT2K_EPI_STORE && !bias) return set_error(GPT2_ERR_INVALID_ARG, "epilogue operand missing");
+    if (epilogue == GPT2K_EPI_BIAS_RESID) {
+        if (!resid) return set_error(GPT2_ERR_INVALID_ARG, "epilogue operand missing");
+        if (out_dtype != GPT2K_F32) return set_error(GPT2_ERR_INVALID_ARG, "bias_resid writes fp32");
+        if (ldr < N) return set_error(GPT2_ERR_INVALID_ARG, "need ldr >= N");
+    }
+    if (misaligned(a_scale, 4) || misaligned(b_scale, 4) || misaligned(out, elem_size(out_dtype)) ||
+        misaligned(bias, 4) || misaligned(resid, 4) || misaligned(status_dev, 4))
+        return set_error(GPT2_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
+    long long launches = 0;
+    Ctx c = kctx(stream, status_dev, &launches);
+    I8Product p;
+    p.A = A;
+    p.lda = lda;
+    p.sa = a_scale;
+    p.B = B;
+    p.ldb = ldb;
+    p.sb = b_scale;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.kind = epilogue;
+    p.out_f32 = out_dtype == GPT2K_F32;
+    p.out = out;
+    p.ldo = ldo;
+    p.bias = bias;
+    p.resid = resid;
+    p.ldr = ldr;
+    if (!launch_matmul_i8(c, p)) return set_error(GPT2_ERR_CUDA, "tensor-map encoding failed");
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return set_error(GPT2_ERR_CUDA, cudaGetErrorString(err));
+    return GPT2_OK;
+}
+
+// ---------------------------------------------------------------- token log-probabilities
+namespace {
+int check_logprob_args(int dtype, const void* logits, int rows, int V, int64_t ld, float temperature,
+                       const uint32_t* status) {
+    if (dtype != GPT2K_F32 && dtype != GPT2K_BF16) return set_error(GPT2_ERR_INVALID_ARG, "unknown dtype");
+    if (rows < 1 || V < 1 || ld < V) return set_error(GPT2_ERR_INVALID_ARG, "need rows, V >= 1 and ld >= V");
+    if (!logits || !status) return set_error(GPT2_ERR_INVALID_ARG, "NULL operand");
+    if (!(temperature > 0.f) || !(temperature < INFINITY) || !(1.f / temperature < INFINITY))
+        return set_error(GPT2_ERR_INVALID_ARG, "temperature must be finite and > 0, as its reciprocal");
+    if (misaligned(logits, elem_size(dtype)) || misaligned(status, 4))
+        return set_error(GPT2_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
+    return GPT2_OK;
+}
+}  // namespace
+
+extern "C" int gpt2k_token_logprobs(int dtype, const void* logits, int rows, int V, int64_t ld, float temperature,
+                                    const int32_t* targets, int top_k, float* logp, float* entropy, float* lse,
+                                    int32_t* top_ids, float* top_logp, uint32_t* status_dev, void* stream) {
+    int rc = check_logprob_args(dtype, logits, rows, V, ld, temperature, status_dev);
+    if (rc) return rc;
+    if ((targets != nullptr) != (logp != nullptr))
+        return set_error(GPT2_ERR_INVALID_ARG, "targets and logp are given together");
+    if (top_k < 0 || top_k > LOGPROB_MAX_TOP || top_k > V)
+        return set_error(GPT2_ERR_INVALID_ARG, "need 0 <= top_k <= min(32, V)");
+    if ((top_k > 0) != (top_ids != nullptr) || (top_k > 0) != (top_logp != nullptr))
+        return set_error(GPT2_ERR_INVALID_ARG, "top_ids and top_logp are given exactly when top_k > 0");
+    if (!logp && !entropy && !lse && !top_k) return set_error(GPT2_ERR_INVALID_ARG, "no output asked for");
+    if (misaligned(targets, 4) || misaligned(logp, 4) || misaligned(entropy, 4) || misaligned(lse, 4) ||
+        misaligned(top_ids, 4) || misaligned(top_logp, 4))
+        return set_error(GPT2_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
+    long long launches = 0;
+    Ctx c = kctx(stream, status_dev, &launches);
+    const LogprobOut o = {logp, entropy, lse, top_ids, top_logp, top_k};
+    if (dtype == GPT2K_F32)
+        launch_token_logprobs<float>(c, (const float*)logits, ld, rows, V, temperature, targets, o);
+    else
+        launch_token_logprobs<bf16>(c, (const bf16*)logits, ld, rows, V, temperature, targets, o);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return set_error(GPT2_ERR_CUDA, cudaGetErrorString(err));
+    return GPT2_OK;
+}
+
+extern "C" int gpt2k_token_logprobs_bwd(int dtype, const void* logits, int rows, int V, int64_t ld, float temperature,
+                                        const int32_t* targets, const float* lse, const float* dlogp,
+                                        const float* entropy, const float* dentropy, void* dlogits, int64_t ldd,
+                                        uint32_t* status_dev, void* stream) {
+    int rc = check_logprob_args(dtype, logits, rows, V, ld, temperature, status_dev);
+    if (rc) return rc;
+    if (ldd < V) return set_error(GPT2_ERR_INVALID_ARG, "need ldd >= V");
+    if (!lse || !dlogits) return set_error(GPT2_ERR_INVALID_ARG, "NULL operand");
+    if (!dlogp && !dentropy) return set_error(GPT2_ERR_INVALID_ARG, "need dlogp or dentropy");
+    if ((dlogp != nullptr) != (targets != nullptr))
+        return set_error(GPT2_ERR_INVALID_ARG, "targets and dlogp are given together");
+    if (dentropy && !entropy) return set_error(GPT2_ERR_INVALID_ARG, "dentropy needs entropy");
+    if (dlogits == logits && ldd != ld)
+        return set_error(GPT2_ERR_INVALID_ARG, "a gradient in place of the logits has their row stride");
+    if (misaligned(dlogits, elem_size(dtype)) || misaligned(targets, 4) || misaligned(lse, 4) ||
+        misaligned(dlogp, 4) || misaligned(entropy, 4) || misaligned(dentropy, 4))
+        return set_error(GPT2_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
+    long long launches = 0;
+    Ctx c = kctx(stream, status_dev, &launches);
+    if (dtype == GPT2K_F32)
+        launch_token_logprobs_bwd<float>(c, (const float*)logits, ld, rows, V, temperature, targets, lse, dlogp,
+                                         entropy, dentropy, (float*)dlogits, ldd);
+    else
+        launch_token_logprobs_bwd<bf16>(c, (const bf16*)logits, ld, rows, V, temperature, targets, lse, dlogp, entropy,
+                                        dentropy, (bf16*)dlogits, ldd);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return set_error(GPT2_ERR_CUDA, cudaGetErrorString(err));
+    return GPT2_OK;
+}

@@ -285,6 +285,56 @@ void launch_copy_tokens(const Ctx& ctx, const int* src, long long src_ld, int* d
                         int cols);
 
 // ----------------------------------------------------------------------------
+// 8-bit linear layers (k_quantize.cu, k_matmul_i8.cu) and token log-probabilities
+// (k_token_logprobs.cu).
+// ----------------------------------------------------------------------------
+// Row r of x (rows x K, stride ldx) -> int8 codes q (stride ldq) and scale[r]; the
+// definition is gpt2k_quantize_rows's.
+template <typename T>
+void launch_quantize_rows(const Ctx& ctx, const T* x, long long ldx, int rows, int K, int8_t* q, long long ldq,
+                          float* scale);
+
+// out(m, n) = epilogue((sum_k A(m, k) B(n, k)) sa[m] sb[n]); A, B int8 row-major with
+// row strides lda, ldb; EPI_STORE, EPI_BIAS, EPI_BIAS_GELU (out only) or
+// EPI_BIAS_RESID (resid has stride ldr); out fp32 (out_f32) or bf16, stride ldo.
+struct I8Product {
+    const int8_t* A;
+    long long lda;
+    const float* sa;
+    const int8_t* B;
+    long long ldb;
+    const float* sb;
+    int M, N, K;
+    int kind, out_f32;
+    void* out;
+    long long ldo;
+    const float* bias;
+    const float* resid;
+    long long ldr;
+};
+constexpr int I8_MAX_K = 131071;   // (2^31 - 1) / 128^2: every sum fits in 32 bits
+bool launch_matmul_i8(const Ctx& ctx, const I8Product& p);
+
+// Results of gpt2k_token_logprobs; NULL members are not computed.
+struct LogprobOut {
+    float* logp;
+    float* entropy;
+    float* lse;
+    int* top_ids;
+    float* top_logp;
+    int top_k;
+};
+constexpr int LOGPROB_MAX_TOP = 32;
+template <typename T>
+void launch_token_logprobs(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float temperature,
+                           const int* targets, const LogprobOut& out);
+// dlogp, entropy, dentropy and targets may be NULL; dlogits may be logits.
+template <typename T>
+void launch_token_logprobs_bwd(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float temperature,
+                               const int* targets, const float* lse, const float* dlogp, const float* entropy,
+                               const float* dentropy, T* dlogits, long long ldd);
+
+// ----------------------------------------------------------------------------
 // Optimiser and parameter utilities.
 // ----------------------------------------------------------------------------
 struct AdamChunk {        // a run of elements inside one tensor

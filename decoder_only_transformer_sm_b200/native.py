@@ -62,7 +62,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise RuntimeError(f"{path} not found: build it with `python -m decoder_only_transformer_sm_b200.build`")
     lib = ctypes.CDLL(path)
-    P, I, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    P, I, F, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_int64
     sig = {
         "gpt2_last_error": (ctypes.c_char_p, []),
         "gpt2_create": (I, [ctypes.POINTER(Config), P, ctypes.POINTER(P)]),
@@ -102,6 +102,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "gpt2k_sample": (I, [I, P, I, I, ctypes.c_int64, F, I, P, P, P, P]),
         "gpt2k_embedding_bwd": (I, [P, P, I, I, I, I, P, P, P, P, P]),
         "gpt2k_embedding_bwd_workspace": (I, [I, I, I, ctypes.POINTER(ctypes.c_int64)]),
+        "gpt2k_quantize_rows": (I, [I, P, I, I, L, P, L, P, P]),
+        "gpt2k_matmul_i8": (I, [P, L, P, P, L, P, I, I, I, I, I, P, L, P, P, L, P, P]),
+        "gpt2k_token_logprobs": (I, [I, P, I, I, L, F, P, I, P, P, P, P, P, P, P]),
+        "gpt2k_token_logprobs_bwd": (I, [I, P, I, I, L, F, P, P, P, P, P, P, L, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -448,3 +452,134 @@ def sample(logits, V: int, temperature: float, top_k: int, u, next_tokens, ld: i
     _check(load_library().gpt2k_sample(_dtype_code(logits), _ptr(logits), rows, V, ld if ld is not None else V,
                                        temperature, top_k, _ptr(u), _ptr(next_tokens), _ptr(status), stream))
     return status
+
+
+# ---------------------------------------------------------------------------
+# 8-bit linear layers and token log-probabilities. Matrices may be views whose
+# rows lie further apart than they are long (unit stride inside a row).
+# ---------------------------------------------------------------------------
+def _rows_of(t, name, dtypes, rows=None, cols=None):
+    """(address, row stride) of a 2-D tensor with unit stride inside its rows."""
+    if t.dim() != 2 or t.dtype not in dtypes:
+        raise ValueError(f"{name}: a 2-D tensor of {' or '.join(str(d) for d in dtypes)} is needed, "
+                         f"got {tuple(t.shape)} {t.dtype}")
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name}: shape {(r, c)} where {(rows or r, cols or c)} is needed")
+    sr, sc = t.stride()
+    if c > 1 and sc != 1:
+        raise ValueError(f"{name}: the elements of a row must lie side by side")
+    return t.data_ptr(), (sr if r > 1 else max(sr, c))
+
+
+def _vector_of(t, name, dtype, n):
+    """Address of a contiguous vector of n elements (None passes NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: {n} contiguous elements of {dtype} are needed, got {tuple(t.shape)} {t.dtype}")
+    return t.data_ptr()
+
+
+class _OnDevice:
+    """Runs a call with the tensors' device current: checks that they share one,
+    and gives the stream (the device's current one, or the caller's) and the
+    status word (made on that stream if the caller has none)."""
+
+    def __init__(self, tensors, status, stream, with_status=True):
+        import torch
+        dev = tensors[0].device
+        if dev.type != "cuda":
+            raise ValueError(f"device tensors are needed, got one on {dev}")
+        for t in tensors:
+            if t is not None and t.device != dev:
+                raise ValueError(f"all tensors must be on one device, got {t.device} and {dev}")
+        if status is not None and status.device != dev:
+            raise ValueError(f"the status word must be on {dev}")
+        self._guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        self.stream = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+        if status is None and with_status:
+            on = torch.cuda.ExternalStream(stream, device=dev) if stream else None
+            with torch.cuda.stream(on):
+                status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.status = status
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self
+
+    def __exit__(self, *a):
+        if self._guard is not None:
+            self._guard.__exit__(*a)
+
+
+def quantize_rows(x, q, scale, stream=None):
+    """gpt2k_quantize_rows: x (rows, K) float32 or bfloat16 -> int8 codes q (rows, K) and scale (rows,) float32."""
+    import torch
+    px, ldx = _rows_of(x, "x", (torch.float32, torch.bfloat16))
+    rows, K = x.shape
+    pq, ldq = _rows_of(q, "q", (torch.int8,), rows, K)
+    ps = _vector_of(scale, "scale", torch.float32, rows)
+    with _OnDevice((x, q, scale), None, stream, with_status=False) as on:
+        _check(load_library().gpt2k_quantize_rows(_dtype_code(x), px, rows, K, ldx, pq, ldq, ps, on.stream))
+
+
+def matmul_i8(A, a_scale, B, b_scale, out, epilogue: str = "store", bias=None, resid=None, status=None, stream=None):
+    """gpt2k_matmul_i8: out (M, N) = epilogue(A (M, K) B (N, K)^T * a_scale (M,) * b_scale (N,)), A and B int8,
+    out float32 or bfloat16, bias (N,) and resid (M, N) float32; returns the status tensor."""
+    import torch
+    pa, lda = _rows_of(A, "A", (torch.int8,))
+    M, K = A.shape
+    pb, ldb = _rows_of(B, "B", (torch.int8,), None, K)
+    N = B.shape[0]
+    po, ldo = _rows_of(out, "out", (torch.float32, torch.bfloat16), M, N)
+    pr, ldr = (None, 0) if resid is None else _rows_of(resid, "resid", (torch.float32,), M, N)
+    psa, psb = _vector_of(a_scale, "a_scale", torch.float32, M), _vector_of(b_scale, "b_scale", torch.float32, N)
+    pbias = _vector_of(bias, "bias", torch.float32, N)
+    with _OnDevice((A, a_scale, B, b_scale, out, bias, resid), status, stream) as on:
+        _check(load_library().gpt2k_matmul_i8(pa, lda, psa, pb, ldb, psb, M, N, K, EPILOGUE[epilogue],
+                                              _dtype_code(out), po, ldo, pbias, pr, ldr, _ptr(on.status), on.stream))
+    return on.status
+
+
+def token_logprobs(logits, V: int, temperature: float, targets=None, logp=None, entropy=None, lse=None, top_ids=None,
+                   top_logp=None, status=None, stream=None):
+    """gpt2k_token_logprobs on rows of logits (rows, >= V; the first V columns), float32 or bfloat16: targets (rows,)
+    int32 with logp, entropy, lse (rows,) float32, top_ids int32 and top_logp float32 (rows, k); what is None is not
+    computed. Returns the status tensor."""
+    import torch
+    px, ld = _rows_of(logits, "logits", (torch.float32, torch.bfloat16))
+    rows = logits.shape[0]
+    if V > logits.shape[1]:
+        raise ValueError(f"V = {V} above the {logits.shape[1]} columns of logits")
+    k = 0 if top_ids is None else top_ids.shape[-1]
+    f32 = torch.float32
+    pt = _vector_of(targets, "targets", torch.int32, rows)
+    pl, pe, ps = (_vector_of(logp, "logp", f32, rows), _vector_of(entropy, "entropy", f32, rows),
+                  _vector_of(lse, "lse", f32, rows))
+    pi, pp = _vector_of(top_ids, "top_ids", torch.int32, rows * k), _vector_of(top_logp, "top_logp", f32, rows * k)
+    with _OnDevice((logits, targets, logp, entropy, lse, top_ids, top_logp), status, stream) as on:
+        _check(load_library().gpt2k_token_logprobs(_dtype_code(logits), px, rows, V, ld, temperature, pt, k, pl, pe,
+                                                   ps, pi, pp, _ptr(on.status), on.stream))
+    return on.status
+
+
+def token_logprobs_bwd(logits, V: int, temperature: float, lse, dlogits, targets=None, dlogp=None, entropy=None,
+                       dentropy=None, status=None, stream=None):
+    """gpt2k_token_logprobs_bwd: dlogits (rows, >= V; the first V columns; logits' type, or logits itself) from
+    dlogp and dentropy (rows,) float32 and the forward's lse and entropy. Returns the status tensor."""
+    import torch
+    px, ld = _rows_of(logits, "logits", (torch.float32, torch.bfloat16))
+    rows = logits.shape[0]
+    pd, ldd = _rows_of(dlogits, "dlogits", (logits.dtype,), rows)
+    if V > min(logits.shape[1], dlogits.shape[1]):
+        raise ValueError(f"V = {V} above the columns of logits or dlogits")
+    f32 = torch.float32
+    pt, pl = _vector_of(targets, "targets", torch.int32, rows), _vector_of(lse, "lse", f32, rows)
+    pg, pe, ph = (_vector_of(dlogp, "dlogp", f32, rows), _vector_of(entropy, "entropy", f32, rows),
+                  _vector_of(dentropy, "dentropy", f32, rows))
+    with _OnDevice((logits, lse, dlogits, targets, dlogp, entropy, dentropy), status, stream) as on:
+        _check(load_library().gpt2k_token_logprobs_bwd(_dtype_code(logits), px, rows, V, ld, temperature, pt, pl, pg,
+                                                       pe, ph, pd, ldd, _ptr(on.status), on.stream))
+    return on.status

@@ -171,6 +171,86 @@ int gpt2k_embedding_bwd(const int32_t* idx, const float* dx, int B, int T, int C
  * INVALID_ARG (B, T or C < 1, floats NULL). */
 int gpt2k_embedding_bwd_workspace(int B, int T, int C, int64_t* floats);
 
+/* ---- 8-bit linear layers --------------------------------------------------
+ * nn.Linear on a trained model's weights with 8-bit operands: weights (N, K)
+ * quantised once by output channel, activations (M, K) by token before each
+ * product, both with gpt2k_quantize_rows. */
+
+/* Symmetric quantisation of each row of x (rows, K) in dtype, row stride ldx
+ * elements: with a = max_k |x[r][k]|,
+ *   scale[r] = a / 127 (fp32, rounded once),
+ *   q[r][k]  = 127 x[r][k] / a rounded to the nearest whole number, ties to
+ *              even (of the exact quotient: the codes depend on no rounding).
+ * q is int8 in [-127, 127], row stride ldq bytes; bytes K .. ldq - 1 of a row are
+ * left as they are. A row of zeros has scale 0 and codes 0; a row with a NaN or
+ * an infinity has scale NaN and codes 0, so that its products are NaN. x and q
+ * may start anywhere an element may; 16-byte aligned rows are fastest. Errors:
+ * INVALID_ARG (unknown dtype, rows or K < 1, a stride below K, a NULL or
+ * misaligned pointer). */
+int gpt2k_quantize_rows(int dtype, const void* x, int rows, int K, int64_t ldx, int8_t* q, int64_t ldq,
+                        float* scale, void* stream);
+
+/* out[m][n] = epilogue( a_scale[m] * b_scale[n] * sum_k A[m][k] B[n][k] )
+ * (the GPT2K_NT layout: y = x W^T). A (M, K), B (N, K) int8, row strides lda,
+ * ldb bytes. The sum is exact (32-bit integers; K <= 131071); it is rounded to
+ * fp32 and multiplied by a_scale[m], then b_scale[n]. Epilogues, in fp32, the
+ * result rounded once to out_dtype (GPT2K_F32 or GPT2K_BF16):
+ *   GPT2K_EPI_STORE      out = u                 (u: the scaled sum)
+ *   GPT2K_EPI_BIAS       out = u + bias[n]
+ *   GPT2K_EPI_BIAS_GELU  out = gelu_tanh(u + bias[n])   (no derivative output)
+ *   GPT2K_EPI_BIAS_RESID out = resid[m][n] + u + bias[n]   (GPT2K_F32 only;
+ *                        resid fp32, row stride ldr; it may be out itself)
+ * out has row stride ldo elements; columns N .. ldo - 1 are left as they are.
+ * out must not overlap A or B. Operands may start anywhere an element may:
+ * A and B whose first byte and row stride are multiples of 16 take the tensor
+ * cores or, for a few rows, the weight-streaming kernel; other ones a slower
+ * kernel. Errors: INVALID_ARG (sizes < 1, K > 131071, a stride below its row,
+ * another epilogue, an operand of the epilogue missing, bias_resid with a bf16
+ * result, a NULL or misaligned pointer). */
+int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B, int64_t ldb,
+                    const float* b_scale, int M, int N, int K, int epilogue, int out_dtype, void* out, int64_t ldo,
+                    const float* bias, const float* resid, int64_t ldr, uint32_t* status_dev, void* stream);
+
+/* ---- Log-probabilities of given tokens ------------------------------------
+ * What the drawing of a token ("GPT-2 from Scratch", "A generation loop") and
+ * the loss see: row r of logits is logits[r * ld .. r * ld + V - 1] in dtype,
+ * z = logits / temperature in fp32 (past fp32's range: an infinity), p =
+ * softmax(z). A z of -inf is a masked token.
+ *   lse[r]     = log sum_v exp(z_v)
+ *   logp[r]    = z[targets[r]] - lse[r]; 0 where targets[r] is -1
+ *   entropy[r] = -sum_v p_v log p_v  (nats; masked tokens add 0)
+ *   top_ids, top_logp (rows, top_k): the top_k largest logits' indices and log
+ *                probabilities, largest first, equal values by lowest index
+ * targets and logp are given together or both NULL; entropy and lse may be
+ * NULL; top_k = 0 and NULL top_ids and top_logp for no alternatives, else
+ * 1 <= top_k <= min(32, V). At least one output. fp32 arithmetic.
+ * A row of which nothing is left (every z = -inf): lse and log probabilities
+ * -inf, entropy 0, ids 0 .. top_k - 1. A row with a NaN or z = +inf: NaN in
+ * lse, entropy, top_logp and a given target's logp; its ids are ordered with
+ * NaN above every number. A target outside [-1, V) sets status bit 0 and is
+ * clamped into [0, V). Errors: INVALID_ARG (unknown dtype, rows or V < 1,
+ * ld < V, a temperature that is not finite and > 0 or whose reciprocal is
+ * infinite, arguments that do not go together, a NULL or misaligned pointer). */
+int gpt2k_token_logprobs(int dtype, const void* logits, int rows, int V, int64_t ld, float temperature,
+                         const int32_t* targets, int top_k, float* logp, float* entropy, float* lse,
+                         int32_t* top_ids, float* top_logp, uint32_t* status_dev, void* stream);
+
+/* Gradient of gpt2k_token_logprobs: for a loss with derivatives dlogp[r] and
+ * dentropy[r] by the row's logp and entropy,
+ *   dlogits[r][v] = (g (1[v = targets[r]] - p_v) - h p_v (log p_v + entropy[r])) / temperature
+ * with g = dlogp[r] (0 where targets[r] is -1), h = dentropy[r],
+ * log p_v = z_v - lse[r]; lse and entropy are those of the forward. Masked
+ * tokens get 0 (a masked target g / temperature). dlogits is in dtype with row
+ * stride ldd, columns V .. ldd - 1 left as they are; it may be logits itself
+ * (with ldd = ld), but not overlap it otherwise. A row with g = h = 0, or lse
+ * -inf, is not read and gets zeros. targets and dlogp are given together or
+ * both NULL, dentropy with entropy; one of dlogp and dentropy is needed.
+ * Targets outside [-1, V) as in the forward. Errors: as the forward. */
+int gpt2k_token_logprobs_bwd(int dtype, const void* logits, int rows, int V, int64_t ld, float temperature,
+                             const int32_t* targets, const float* lse, const float* dlogp, const float* entropy,
+                             const float* dentropy, void* dlogits, int64_t ldd, uint32_t* status_dev,
+                             void* stream);
+
 #ifdef __cplusplus
 }
 #endif
