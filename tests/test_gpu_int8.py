@@ -137,7 +137,8 @@ def _product(M, N, K, epilogue, out_dtype, pads=(0, 0, 0, 0), shift=(0, 0, 0), s
 
 SIZES = [(1, 1, 1), (1, 8, 16), (2, 100, 768), (3, 50, 31), (4, 1024, 128), (5, 77, 96), (8, 2304, 768), (8, 130, 1616),
          (9, 64, 64), (16, 8, 16), (17, 129, 144), (64, 256, 128), (127, 300, 272), (128, 128, 128), (129, 257, 160),
-         (333, 1600, 1600), (256, 40, 4096), (700, 96, 32), (1, 5001, 2048), (7, 33, 5000)]
+         (333, 1600, 1600), (256, 40, 4096), (700, 96, 32), (1, 5001, 2048), (7, 33, 5000),
+         (640, 1920, 96), (1000, 2403, 144), (2305, 2310, 272)]   # more tiles than SMs at each tile width
 
 
 @pytest.mark.parametrize("epilogue,out_dtype", [("store", torch.bfloat16), ("store", torch.float32),
