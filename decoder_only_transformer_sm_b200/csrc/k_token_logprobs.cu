@@ -2,119 +2,342 @@
 // gradient ("GPT-2 from Scratch", "A generation loop": the distribution a token is
 // drawn from is softmax(logits / temperature)).
 //
-// With z = x / tau, m = max z, d = z - m, s = sum e^d, w = sum e^d d:
-//   lse = m + log s,   log p_v = d_v - log s,   H = -sum p log p = log s - w / s.
-// Masked logits are -inf: they add nothing to s and w. A row of which nothing is
-// left (m = -inf) has lse = log p = -inf and H = 0; a row with NaN or +inf has NaN
-// in all of them.
+// With c = log2(e) / tau, m = max x, d = x - m, s = sum 2^(c d), w = sum 2^(c d) d:
+//   lse = m / tau + log s,   log p_v = d_v / tau - log s,   H = -sum p log p = log s - w / (tau s).
+// Differences to the maximum are taken before they are scaled, so the terms that
+// count carry the smallest errors. Masked logits are -inf: they add nothing to s and
+// w. A row of which nothing is left has lse = log p = -inf and H = 0; a row with NaN or
+// +inf has NaN in all of them.
+//
+// Forward: one pass over the row. A thread keeps a running (m, s, w) and rescales
+// it when a load of several vectors raises m; the block's threads, and with few rows
+// the blocks of a cluster (distributed shared memory), join theirs at the end.
+// Top alternatives come from the same pass: four neighbouring lanes share a group,
+// whose largest value is known at the end. A group is read again (from L2) only if
+// fewer than top_k groups have a larger maximum: no other group can hold one of the
+// top_k, and their smallest maximum is a bound that few other values pass. What passes it is
+// merged in sorted lists of 64-bit keys (value, then lowest index), one list a warp.
+#include <cooperative_groups.h>
+
 #include "kernels.cuh"
 
 namespace gpt2 {
 
 namespace {
 
-constexpr float NEG_INF = -__builtin_huge_valf();
+namespace cg = cooperative_groups;
+typedef unsigned long long u64;
 
-// 64-bit keys whose order is that of (value, then lowest index): the value's bits
-// turned into an unsigned order (-0 as +0, NaN above everything), then ~index. No
-// entry has the key 0 or all ones.
-__device__ __forceinline__ unsigned long long order_key(float x, int v) {
-    unsigned b = __float_as_uint(x + 0.f);
-    b = (b & 0x80000000u) ? ~b : b | 0x80000000u;
-    if (x != x) b = 0xffc00000u;   // above +inf, and no key is all ones
-    return ((unsigned long long)b << 32) | (unsigned)~v;
+constexpr float NEG_INF = -__builtin_huge_valf();
+constexpr float LOG2E = 1.4426950408889634f;
+__device__ __forceinline__ float nan_value() { return __uint_as_float(0x7fc00000u); }
+
+// Unsigned numbers whose order is that of the values: -0 as +0, NaN above +inf. No value has 0 or all ones.
+__device__ __forceinline__ unsigned order_of(float x) {
+    const unsigned b = __float_as_uint(x + 0.f);
+    if (x != x) return 0xffc00000u;
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(unsigned o) {
+    if (o == 0xffc00000u) return nan_value();
+    return __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
+}
+// Larger value first, then lower index.
+__device__ __forceinline__ u64 key_of(unsigned order, int v) { return ((u64)order << 32) | (unsigned)~v; }
+
+// A row of V elements as vectors of 16 bytes: vector 0 holds the elements before the first
+// 16-byte boundary (0 .. N - 1 of them), vectors 1 .. full are whole, vector full + 1 the rest.
+template <typename T>
+struct RowVecs {
+    static constexpr int N = 16 / sizeof(T);
+    int head, full, V;
+    __device__ __forceinline__ RowVecs(const T* row, int V_) : V(V_) {
+        head = min(V, (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(T));
+        full = (V - head) / N;
+    }
+    __device__ __forceinline__ int count() const { return full + 2; }
+    __device__ __forceinline__ int first(int i) const { return i == 0 ? 0 : head + (i - 1) * N; }
+    __device__ __forceinline__ int last(int i) const { return i == 0 ? head : min(V, head + i * N); }
+    __device__ __forceinline__ bool whole(int i) const { return (unsigned)(i - 1) < (unsigned)full; }
+};
+
+__device__ __forceinline__ void unpack(const uint4& q, float (&f)[8], bf16) {
+    const unsigned u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const uint4& q, float (&f)[4], float) {
+    f[0] = __uint_as_float(q.x);
+    f[1] = __uint_as_float(q.y);
+    f[2] = __uint_as_float(q.z);
+    f[3] = __uint_as_float(q.w);
 }
 
+// Vector i's bits; what lies outside the row (and a vector past the end) is -inf.
 template <typename T>
-__global__ void __launch_bounds__(256) token_logprobs_kernel(const T* __restrict__ logits, long long ld, int V,
-                                                             float inv_tau, const int* __restrict__ targets,
-                                                             LogprobOut out, unsigned* status) {
-    __shared__ float red[3][8];
-    __shared__ unsigned long long best[8];
-    const int row = blockIdx.x, tid = threadIdx.x;
+__device__ __forceinline__ uint4 load_vec(const T* row, const RowVecs<T>& rv, int i, int end) {
+    constexpr unsigned NONE = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+    uint4 q = make_uint4(NONE, NONE, NONE, NONE);
+    if (i < end) {
+        if (rv.whole(i)) return __ldg(reinterpret_cast<const uint4*>(row + rv.head) + (i - 1));
+        union {
+            uint4 q;
+            T t[RowVecs<T>::N];
+        } u;
+        u.q = q;
+        const int a = rv.first(i), b = rv.last(i);
+#pragma unroll
+        for (int j = 0; j < RowVecs<T>::N; ++j)
+            if (a + j < b) u.t[j] = row[a + j];
+        q = u.q;
+    }
+    return q;
+}
+
+struct Sums {
+    float m, s, w;   // m = -FLT_MAX and s = 0 where nothing was seen
+    __device__ __forceinline__ void raise(float to, float c) {
+        const float r = ex2_approx((m - to) * c);
+        w = (w - fminf(to - m, 1e30f) * s) * r;   // s is 0 or the difference finite enough
+        s *= r;
+        m = to;
+    }
+    __device__ __forceinline__ void join(Sums o, float c) {
+        const float to = fmaxf(m, o.m);
+        raise(to, c);
+        o.raise(to, c);
+        s += o.s;
+        w += o.w;
+    }
+    __device__ __forceinline__ Sums shuffled(int mask) const {
+        return {__shfl_xor_sync(0xffffffffu, m, mask), __shfl_xor_sync(0xffffffffu, s, mask),
+                __shfl_xor_sync(0xffffffffu, w, mask)};
+    }
+};
+
+// Inserts the keys that `pass` lanes hold into the warp's descending list (lane i: the
+// i-th largest, 0 for none).
+__device__ __forceinline__ void insert(u64& list, u64 key, bool pass) {
+    const int lane = threadIdx.x & 31;
+    for (unsigned todo = __ballot_sync(0xffffffffu, pass); todo; todo &= todo - 1) {
+        const u64 k = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
+        const int at = __popc(__ballot_sync(0xffffffffu, list > k));
+        const u64 up = __shfl_up_sync(0xffffffffu, list, 1);
+        if (lane == at) list = k;
+        else if (lane > at) list = up;
+    }
+}
+
+template <int NT>
+struct ForwardSmem {
+    alignas(16) unsigned group[NT / 4];   // order of each group's largest value
+    u64 cand[NT];                         // the warps' lists, packed
+    Sums sums[NT / 32];
+    unsigned bound;
+    int n_cand;
+    // of the cluster's first block: every block's results
+    Sums all_sums[8];
+    u64 all_top[8 * LOGPROB_MAX_TOP];
+};
+
+// Ranks n keys in shared memory; rank(i, key) is called for those among the k largest.
+template <typename F>
+__device__ __forceinline__ void for_top(const u64* keys, int n, int k, int nt, F rank) {
+    for (int i = threadIdx.x; i < n; i += nt) {
+        const u64 mine = keys[i];
+        if (mine == 0) continue;
+        int above = 0;
+        for (int j = 0; j < n; ++j) above += keys[j] > mine;
+        if (above < k) rank(above, mine);
+    }
+}
+
+template <typename T, int NT, bool CLUSTER>
+__global__ void __launch_bounds__(NT) token_logprobs_kernel(const T* __restrict__ logits, long long ld, int V,
+                                                            float inv_tau, const int* __restrict__ targets,
+                                                            LogprobOut out, int parts, unsigned* status) {
+    constexpr int N = RowVecs<T>::N, U = 4;
+    __shared__ ForwardSmem<NT> sm;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int row = CLUSTER ? blockIdx.x / parts : blockIdx.x, part = CLUSTER ? blockIdx.x % parts : 0;
     const T* x = logits + (long long)row * ld;
-    float m = NEG_INF;
-    bool nan = false;
-    for (int v = tid; v < V; v += 256) {
-        const float z = to_f(x[v]) * inv_tau;
-        nan |= z != z;
-        m = fmaxf(m, z);
-    }
-    m = warp_max(m);
-    nan = __syncthreads_or(nan);
-    if ((tid & 31) == 0) red[0][tid >> 5] = m;
-    __syncthreads();
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, red[0][i]);
-    const bool empty = m == NEG_INF && !nan, bad = nan || m == -NEG_INF;
-    const float m0 = empty || bad ? 0.f : m;
-    float s = 0.f, w = 0.f;
-    for (int v = tid; v < V; v += 256) {
-        const float d = to_f(x[v]) * inv_tau - m0;
-        const float e = expf(d);
-        s += e;
-        if (e > 0.f) w += e * d;
-    }
-    s = warp_sum(s);
-    w = warp_sum(w);
-    if ((tid & 31) == 0) {
-        red[1][tid >> 5] = s;
-        red[2][tid >> 5] = w;
-    }
-    __syncthreads();
-    s = w = 0.f;
-    for (int i = 0; i < 8; ++i) {
-        s += red[1][i];
-        w += red[2][i];
-    }
-    const float log_s = logf(s);
-    const float nanv = __uint_as_float(0x7fc00000u);
-    auto settle = [&](float v, float nothing) { return bad ? nanv : empty ? nothing : v; };
+    const RowVecs<T> rv(x, V);
+    const int per = CLUSTER ? ceil_div(rv.count(), parts) : rv.count();
+    const int begin = part * per, end = min(rv.count(), begin + per);
+    const float c = LOG2E * inv_tau;
+    if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     if (tid == 0) {
-        if (out.lse) out.lse[row] = settle(m + log_s, NEG_INF);
-        if (out.entropy) out.entropy[row] = settle(log_s - w / s, 0.f);
+        sm.bound = 0xffffffffu;
+        sm.n_cand = 0;
+    }
+
+    Sums a = {-3.402823466e38f, 0.f, 0.f};
+    float largest = NEG_INF;
+    for (int i = begin + tid; i < end; i += U * NT) {
+        uint4 q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[u] = load_vec(x, rv, i + u * NT, end);
+        float f[U][N];
+        float top = NEG_INF;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            unpack(q[u], f[u], T());
+#pragma unroll
+            for (int j = 0; j < N; ++j) top = fmaxf(top, f[u][j]);
+        }
+        largest = fmaxf(largest, top);
+        if (top > a.m) a.raise(top, c);
+        const f32x2 m2 = pk2(-a.m, -a.m), c2 = pk2(c, c);
+        f32x2 s2 = pk2(a.s, 0.f), w2 = pk2(a.w, 0.f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int j = 0; j < N; j += 2) {
+                const f32x2 d2 = add2(pk2(f[u][j], f[u][j + 1]), m2);
+                float y0, y1, d0, d1;
+                upk2(mul2(d2, c2), y0, y1);
+                upk2(d2, d0, d1);
+                const f32x2 e2 = pk2(ex2_approx(y0), ex2_approx(y1));
+                s2 = add2(s2, e2);
+                // a masked value has e = 0 and d = -inf
+                w2 = fma2(e2, pk2(fmaxf(d0, -1e30f), fmaxf(d1, -1e30f)), w2);
+            }
+        }
+        float s0, s1, w0, w1;
+        upk2(s2, s0, s1);
+        upk2(w2, w0, w1);
+        a.s = s0 + s1;
+        a.w = w0 + w1;
+    }
+
+    if (out.top_k) {
+        unsigned order = largest == NEG_INF ? 0u : order_of(largest);
+        if (largest == NEG_INF && begin + tid < end) order = order_of(NEG_INF);
+        if (a.s != a.s) {   // a NaN, or +inf: find out which
+            for (int i = begin + tid; i < end; i += NT)
+                for (int v = rv.first(i); v < rv.last(i); ++v) order = max(order, order_of(to_f(x[v])));
+        }
+        order = max(order, __shfl_xor_sync(0xffffffffu, order, 1));
+        order = max(order, __shfl_xor_sync(0xffffffffu, order, 2));
+        if ((tid & 3) == 0) sm.group[tid >> 2] = order;
+        __syncthreads();
+        int above = 0;
+#pragma unroll
+        for (int j = 0; j < NT / 4; j += 4) {
+            const uint4 g = *reinterpret_cast<const uint4*>(sm.group + j);
+            above += (g.x > order) + (g.y > order) + (g.z > order) + (g.w > order);
+        }
+        const bool again = above < out.top_k;
+        if (again && (tid & 3) == 0) atomicMin(&sm.bound, order);
+        __syncthreads();
+        const unsigned bound = sm.bound;
+        u64 list = 0;
+        // 32 lanes read a group's four vectors (one step of the pass), or two steps' of them
+        constexpr int STEPS = 32 / (4 * N);
+        for (unsigned todo = __ballot_sync(0xffffffffu, again && (tid & 3) == 0); todo; todo &= todo - 1) {
+            const int g0 = (tid & ~31) + __ffs(todo) - 1;
+            const int mine = g0 + (lane / N) % 4, j = lane % N;
+            constexpr int R = 8;
+            for (int i0 = begin; i0 < end; i0 += R * STEPS * NT) {
+                float v[R];
+                int at[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int i = i0 + (r * STEPS + lane / (4 * N)) * NT + mine;
+                    at[r] = -1;
+                    v[r] = 0.f;
+                    if (i < end) {
+                        const int e = rv.first(i) + j;
+                        if (e < rv.last(i)) {
+                            at[r] = e;
+                            v[r] = to_f(x[e]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const unsigned o = order_of(v[r]);
+                    const u64 k = key_of(o, at[r]);
+                    // at most top_k of the list can be among the row's
+                    const u64 least = __shfl_sync(0xffffffffu, list, out.top_k - 1);
+                    insert(list, k, at[r] >= 0 && o >= bound && k > least);
+                }
+            }
+        }
+        const unsigned kept = __ballot_sync(0xffffffffu, list != 0 && lane < out.top_k);
+        int base = 0;
+        if (lane == 0 && kept) base = atomicAdd(&sm.n_cand, __popc(kept));
+        base = __shfl_sync(0xffffffffu, base, 0);
+        if ((kept >> lane) & 1) sm.cand[base + __popc(kept & ((1u << lane) - 1))] = list;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int o = 16; o; o >>= 1) a.join(a.shuffled(o), c);
+    if (lane == 0) sm.sums[tid >> 5] = a;
+    __syncthreads();
+    a = sm.sums[0];
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) a.join(sm.sums[w], c);
+    const u64* keys = sm.cand;
+    int n_keys = out.top_k ? sm.n_cand : 0;
+    if (CLUSTER) {
+        auto cluster = cg::this_cluster();
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // every block has started
+        ForwardSmem<NT>* first = cluster.map_shared_rank(&sm, 0);
+        if (tid == 0) first->all_sums[part] = a;
+        if (out.top_k) {
+            if (tid < out.top_k && tid >= n_keys) first->all_top[part * out.top_k + tid] = 0;
+            for_top(sm.cand, n_keys, out.top_k, NT, [&](int r, u64 k) { first->all_top[part * out.top_k + r] = k; });
+        }
+        cluster.sync();
+        if (part != 0) return;
+        a = sm.all_sums[0];
+        for (int i = 1; i < parts; ++i) a.join(sm.all_sums[i], c);
+        keys = sm.all_top;
+        n_keys = parts * out.top_k;
+    }
+    const float z_max = a.m * inv_tau;
+    const bool bad = a.s != a.s || z_max == -NEG_INF, empty = !bad && (a.s == 0.f || z_max == NEG_INF);
+    const float log_s = logf(a.s);
+    auto settle = [&](float v, float nothing) { return bad ? nan_value() : empty ? nothing : v; };
+    auto logp_of = [&](float v) { return settle((v - a.m) * inv_tau - log_s, NEG_INF); };
+    if (tid == 0) {
+        if (out.lse) out.lse[row] = settle(z_max + log_s, NEG_INF);
+        if (out.entropy) out.entropy[row] = settle(log_s - a.w / a.s * inv_tau, 0.f);
         if (out.logp) {
             int t = targets[row];
             if (t < -1 || t >= V) {
                 atomicOr(status, STATUS_BAD_TOKEN);
                 t = min(max(t, 0), V - 1);
             }
-            out.logp[row] = t < 0 ? 0.f : settle(to_f(x[t]) * inv_tau - m0 - log_s, NEG_INF);
+            out.logp[row] = t < 0 ? 0.f : logp_of(to_f(x[t]));
         }
     }
-    unsigned long long below = ~0ull;
-    for (int j = 0; j < out.top_k; ++j) {
-        unsigned long long k = 0;
-        for (int v = tid; v < V; v += 256) {
-            const unsigned long long c = order_key(to_f(x[v]), v);
-            if (c < below && c > k) k = c;
-        }
-        for (int o = 16; o; o >>= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, o));
-        __syncthreads();
-        if ((tid & 31) == 0) best[tid >> 5] = k;
-        __syncthreads();
-        for (int i = 0; i < 8; ++i) k = max(k, best[i]);
-        below = k;
-        if (tid == 0) {
-            const int v = (int)~(unsigned)k;
-            out.top_ids[(long long)row * out.top_k + j] = v;
-            out.top_logp[(long long)row * out.top_k + j] = settle(to_f(x[v]) * inv_tau - m0 - log_s, NEG_INF);
-        }
-    }
+    for_top(keys, n_keys, out.top_k, NT, [&](int r, u64 k) {
+        out.top_ids[(long long)row * out.top_k + r] = (int)~(unsigned)k;
+        out.top_logp[(long long)row * out.top_k + r] = logp_of(value_of((unsigned)(k >> 32)));
+    });
 }
 
 // dx_v = (1/tau) [ g (1[v = t] - p_v) - h p_v (log p_v + H) ], g = dlogp (0 at an ignored
-// target), h = dentropy; p_v = e^(z_v - lse). Where p_v is 0 only the target's g is left.
+// target), h = dentropy; with d = z_v - lse: p = e^d, and where p is 0 only the target's g is
+// left. One pass, bound by reading x and writing dx; a block takes a run of vectors of a row.
+// dx may be x: a thread writes only what it has read.
 template <typename T>
-__global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* logits, long long ld, int V, float inv_tau,
+__global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, long long ld, int V, float inv_tau,
                                                                  const int* __restrict__ targets,
                                                                  const float* __restrict__ lse,
                                                                  const float* __restrict__ dlogp,
                                                                  const float* __restrict__ entropy,
-                                                                 const float* __restrict__ dentropy, T* dlogits,
-                                                                 long long ldd, unsigned* status) {
-    const int row = blockIdx.x;
-    const T* x = logits + (long long)row * ld;
-    T* dx = dlogits + (long long)row * ldd;
+                                                                 const float* __restrict__ dentropy, T* dx0,
+                                                                 long long ldd, int parts, unsigned* status) {
+    constexpr int N = RowVecs<T>::N, U = 4;
+    const int row = blockIdx.x / parts, part = blockIdx.x % parts;
+    const T* x = x0 + (long long)row * ld;
+    T* dx = dx0 + (long long)row * ldd;
     int t = targets ? targets[row] : -1;
     if (t < -1 || t >= V) {
         if (threadIdx.x == 0) atomicOr(status, STATUS_BAD_TOKEN);
@@ -122,18 +345,86 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* logits
     }
     const float L = lse[row];
     const float g = dlogp && t >= 0 ? dlogp[row] : 0.f, h = dentropy ? dentropy[row] : 0.f;
-    const float H = dentropy ? entropy[row] : 0.f;
+    const float H = h != 0.f ? entropy[row] : 0.f;
     const bool none = (g == 0.f && h == 0.f) || L == NEG_INF;
-    for (int v = threadIdx.x; v < V; v += 256) {
-        float r = 0.f;
+    const float gt = g * inv_tau, A = -(g + h * H) * inv_tau, B = -h * inv_tau;
+    const RowVecs<T> rv(dx, V);   // the vectors of what is written
+    const bool same = (((uintptr_t)x ^ (uintptr_t)dx) & 15) == 0;
+    const int per = ceil_div(rv.count(), parts), end = min(rv.count(), (part + 1) * per);
+    for (int i = part * per + threadIdx.x; i < end; i += U * 256) {
+        union V16 {
+            uint4 q;
+            T t[N];
+            __device__ V16() {}
+        } v[U];
         if (!none) {
-            const float d = fmaf(to_f(x[v]), inv_tau, -L);
-            const float p = expf(d);
-            if (!(p == 0.f)) r = -p * (g + h * (d + H));
-            if (v == t) r += g;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = i + u * 256;
+                if (k < end && rv.whole(k) && same) {
+                    v[u].q = *(reinterpret_cast<const uint4*>(x + rv.head) + (k - 1));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) v[u].t[j] = k < end && rv.first(k) + j < rv.last(k) ? x[rv.first(k) + j] : from_f<T>(0.f);
+                }
+            }
         }
-        dx[v] = from_f<T>(r * inv_tau);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = i + u * 256;
+            if (k >= end) break;
+            const int first = rv.first(k);
+            if (none) {
+                v[u].q = make_uint4(0, 0, 0, 0);
+            } else {
+                float r[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const float d = fmaf(to_f(v[u].t[j]), inv_tau, -L);
+                    const float p = ex2_approx(d * LOG2E);
+                    r[j] = p * fmaf(B, fmaxf(d, -1e30f), A);   // a masked value: p = 0, d = -inf
+                }
+                if ((unsigned)(t - first) < (unsigned)N) {
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        if (first + j == t) r[j] += gt;
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j) v[u].t[j] = from_f<T>(r[j]);
+            }
+            if (rv.whole(k)) {
+                *(reinterpret_cast<uint4*>(dx + rv.head) + (k - 1)) = v[u].q;
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (first + j < rv.last(k)) dx[first + j] = v[u].t[j];
+            }
+        }
     }
+}
+
+template <typename T, int NT>
+void launch_forward(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float inv_tau, const int* targets,
+                    const LogprobOut& out) {
+    // few rows: as many blocks a row as give every SM two, while a thread still has a vector
+    int parts = 8;
+    while (parts > 1 && ((long long)rows * parts > 2 * ctx.num_sms || V < parts * NT * RowVecs<T>::N)) parts /= 2;
+    if (parts == 1) {
+        token_logprobs_kernel<T, NT, false><<<rows, NT, 0, ctx.stream>>>(logits, ld, V, inv_tau, targets, out, 1,
+                                                                         ctx.status);
+        return;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(rows * parts);
+    cfg.blockDim = dim3(NT);
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = parts;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, NT, true>, logits, ld, V, inv_tau, targets, out, parts, ctx.status);
 }
 
 }  // namespace
@@ -141,7 +432,10 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* logits
 template <typename T>
 void launch_token_logprobs(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float temperature,
                            const int* targets, const LogprobOut& out) {
-    token_logprobs_kernel<T><<<rows, 256, 0, ctx.stream>>>(logits, ld, V, 1.f / temperature, targets, out, ctx.status);
+    if (V >= 4096)
+        launch_forward<T, 256>(ctx, logits, ld, rows, V, 1.f / temperature, targets, out);
+    else
+        launch_forward<T, 128>(ctx, logits, ld, rows, V, 1.f / temperature, targets, out);
     ++*ctx.launches;
 }
 
@@ -149,8 +443,10 @@ template <typename T>
 void launch_token_logprobs_bwd(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float temperature,
                                const int* targets, const float* lse, const float* dlogp, const float* entropy,
                                const float* dentropy, T* dlogits, long long ldd) {
-    token_logprobs_bwd_kernel<T><<<rows, 256, 0, ctx.stream>>>(logits, ld, V, 1.f / temperature, targets, lse, dlogp,
-                                                               entropy, dentropy, dlogits, ldd, ctx.status);
+    const int parts = ceil_div(V / RowVecs<T>::N + 2, 1024);   // four vectors a thread
+    token_logprobs_bwd_kernel<T><<<rows * parts, 256, 0, ctx.stream>>>(logits, ld, V, 1.f / temperature, targets, lse,
+                                                                       dlogp, entropy, dentropy, dlogits, ldd, parts,
+                                                                       ctx.status);
     ++*ctx.launches;
 }
 

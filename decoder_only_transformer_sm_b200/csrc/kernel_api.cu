@@ -284,8 +284,10 @@ int check_logprob_args(int dtype, const void* logits, int rows, int V, int64_t l
     if (dtype != GPT2K_F32 && dtype != GPT2K_BF16) return set_error(GPT2_ERR_INVALID_ARG, "unknown dtype");
     if (rows < 1 || V < 1 || ld < V) return set_error(GPT2_ERR_INVALID_ARG, "need rows, V >= 1 and ld >= V");
     if (!logits || !status) return set_error(GPT2_ERR_INVALID_ARG, "NULL operand");
-    if (!(temperature > 0.f) || !(temperature < INFINITY) || !(1.f / temperature < INFINITY))
-        return set_error(GPT2_ERR_INVALID_ARG, "temperature must be finite and > 0, as its reciprocal");
+    if (!(temperature > 0.f) || !(temperature < INFINITY) || !(1.5f / temperature < INFINITY))
+        return set_error(GPT2_ERR_INVALID_ARG, "temperature must be finite and > 0, 1.5 / temperature finite");
+    if ((long long)rows * (V / 2048 + 1) > 0x7fffffffll)
+        return set_error(GPT2_ERR_INVALID_ARG, "rows x V is more than one launch takes");
     if (misaligned(logits, elem_size(dtype)) || misaligned(status, 4))
         return set_error(GPT2_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
     return GPT2_OK;

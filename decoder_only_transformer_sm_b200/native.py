@@ -458,18 +458,33 @@ def sample(logits, V: int, temperature: float, top_k: int, u, next_tokens, ld: i
 # 8-bit linear layers and token log-probabilities. Matrices may be views whose
 # rows lie further apart than they are long (unit stride inside a row).
 # ---------------------------------------------------------------------------
-def _rows_of(t, name, dtypes, rows=None, cols=None):
-    """(address, row stride) of a 2-D tensor with unit stride inside its rows."""
-    if t.dim() != 2 or t.dtype not in dtypes:
-        raise ValueError(f"{name}: a 2-D tensor of {' or '.join(str(d) for d in dtypes)} is needed, "
+# Small calls are bound by the host, so the checks below read each tensor property once.
+_torch = None       # the module and its type codes, set by the first call
+_FLOATS = _INT8 = None
+
+
+def _import_torch():
+    global _torch, _FLOATS, _INT8
+    import torch
+    _FLOATS = {torch.float32: 0, torch.bfloat16: 1}
+    _INT8 = {torch.int8: 0}
+    _torch = torch
+    return torch
+
+
+def _rows_of(t, name, codes, rows=None, cols=None):
+    """(rows, columns, address, row stride, type code) of a 2-D tensor with unit stride inside its rows."""
+    code = codes.get(t.dtype)
+    if code is None or t.dim() != 2:
+        raise ValueError(f"{name}: a 2-D tensor of {' or '.join(str(d) for d in codes)} is needed, "
                          f"got {tuple(t.shape)} {t.dtype}")
     r, c = t.shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{name}: shape {(r, c)} where {(rows or r, cols or c)} is needed")
     sr, sc = t.stride()
-    if c > 1 and sc != 1:
+    if sc != 1 and c > 1:
         raise ValueError(f"{name}: the elements of a row must lie side by side")
-    return t.data_ptr(), (sr if r > 1 else max(sr, c))
+    return r, c, t.data_ptr(), (sr if r > 1 else max(sr, c)), code
 
 
 def _vector_of(t, name, dtype, n):
@@ -481,66 +496,70 @@ def _vector_of(t, name, dtype, n):
     return t.data_ptr()
 
 
-class _OnDevice:
-    """Runs a call with the tensors' device current: checks that they share one,
-    and gives the stream (the device's current one, or the caller's) and the
-    status word (made on that stream if the caller has none)."""
+def _device_of(first, *rest):
+    """Index of the one device that the tensors are on."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError(f"device tensors are needed, got one on {first.device}")
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"all tensors must be on one device, got {t.device} and {first.device}")
+    return dev
 
-    def __init__(self, tensors, status, stream, with_status=True):
-        import torch
-        dev = tensors[0].device
-        if dev.type != "cuda":
-            raise ValueError(f"device tensors are needed, got one on {dev}")
-        for t in tensors:
-            if t is not None and t.device != dev:
-                raise ValueError(f"all tensors must be on one device, got {t.device} and {dev}")
-        if status is not None and status.device != dev:
-            raise ValueError(f"the status word must be on {dev}")
-        self._guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-        self.stream = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
-        if status is None and with_status:
-            on = torch.cuda.ExternalStream(stream, device=dev) if stream else None
-            with torch.cuda.stream(on):
-                status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.status = status
 
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self
+def _status_on(dev, stream):
+    """A cleared status word, made on the stream that the kernel will run on."""
+    on = _torch.cuda.ExternalStream(stream, device=dev) if stream else None
+    with _torch.cuda.device(dev), _torch.cuda.stream(on):
+        return _torch.zeros(1, dtype=_torch.int32, device=dev)
 
-    def __exit__(self, *a):
-        if self._guard is not None:
-            self._guard.__exit__(*a)
+
+def _call(dev, fn, *args):
+    """fn(*args) with device dev current; raises on an error code."""
+    if _torch.cuda.current_device() == dev:
+        rc = fn(*args)
+    else:
+        with _torch.cuda.device(dev):
+            rc = fn(*args)
+    if rc != GPT2_OK:
+        _check(rc)
 
 
 def quantize_rows(x, q, scale, stream=None):
     """gpt2k_quantize_rows: x (rows, K) float32 or bfloat16 -> int8 codes q (rows, K) and scale (rows,) float32."""
-    import torch
-    px, ldx = _rows_of(x, "x", (torch.float32, torch.bfloat16))
-    rows, K = x.shape
-    pq, ldq = _rows_of(q, "q", (torch.int8,), rows, K)
+    torch = _torch or _import_torch()
+    rows, K, px, ldx, code = _rows_of(x, "x", _FLOATS)
+    _, _, pq, ldq, _ = _rows_of(q, "q", _INT8, rows, K)
     ps = _vector_of(scale, "scale", torch.float32, rows)
-    with _OnDevice((x, q, scale), None, stream, with_status=False) as on:
-        _check(load_library().gpt2k_quantize_rows(_dtype_code(x), px, rows, K, ldx, pq, ldq, ps, on.stream))
+    dev = _device_of(x, q, scale)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    _call(dev, (_lib or load_library()).gpt2k_quantize_rows, code, px, rows, K, ldx, pq, ldq, ps, stream)
 
 
 def matmul_i8(A, a_scale, B, b_scale, out, epilogue: str = "store", bias=None, resid=None, status=None, stream=None):
     """gpt2k_matmul_i8: out (M, N) = epilogue(A (M, K) B (N, K)^T * a_scale (M,) * b_scale (N,)), A and B int8,
     out float32 or bfloat16, bias (N,) and resid (M, N) float32; returns the status tensor."""
-    import torch
-    pa, lda = _rows_of(A, "A", (torch.int8,))
-    M, K = A.shape
-    pb, ldb = _rows_of(B, "B", (torch.int8,), None, K)
-    N = B.shape[0]
-    po, ldo = _rows_of(out, "out", (torch.float32, torch.bfloat16), M, N)
-    pr, ldr = (None, 0) if resid is None else _rows_of(resid, "resid", (torch.float32,), M, N)
-    psa, psb = _vector_of(a_scale, "a_scale", torch.float32, M), _vector_of(b_scale, "b_scale", torch.float32, N)
-    pbias = _vector_of(bias, "bias", torch.float32, N)
-    with _OnDevice((A, a_scale, B, b_scale, out, bias, resid), status, stream) as on:
-        _check(load_library().gpt2k_matmul_i8(pa, lda, psa, pb, ldb, psb, M, N, K, EPILOGUE[epilogue],
-                                              _dtype_code(out), po, ldo, pbias, pr, ldr, _ptr(on.status), on.stream))
-    return on.status
+    torch = _torch or _import_torch()
+    f32 = torch.float32
+    M, K, pa, lda, _ = _rows_of(A, "A", _INT8)
+    N, _, pb, ldb, _ = _rows_of(B, "B", _INT8, None, K)
+    _, _, po, ldo, code = _rows_of(out, "out", _FLOATS, M, N)
+    pr, ldr = None, 0
+    if resid is not None:
+        _, _, pr, ldr, code_r = _rows_of(resid, "resid", _FLOATS, M, N)
+        if code_r != 0:
+            raise ValueError("resid: float32 is needed")
+    psa, psb = _vector_of(a_scale, "a_scale", f32, M), _vector_of(b_scale, "b_scale", f32, N)
+    pbias = _vector_of(bias, "bias", f32, N)
+    dev = _device_of(A, a_scale, B, b_scale, out, bias, resid, status)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    if status is None:
+        status = _status_on(dev, stream)
+    _call(dev, (_lib or load_library()).gpt2k_matmul_i8, pa, lda, psa, pb, ldb, psb, M, N, K, EPILOGUE[epilogue],
+          code, po, ldo, pbias, pr, ldr, status.data_ptr(), stream)
+    return status
 
 
 def token_logprobs(logits, V: int, temperature: float, targets=None, logp=None, entropy=None, lse=None, top_ids=None,
@@ -548,38 +567,45 @@ def token_logprobs(logits, V: int, temperature: float, targets=None, logp=None, 
     """gpt2k_token_logprobs on rows of logits (rows, >= V; the first V columns), float32 or bfloat16: targets (rows,)
     int32 with logp, entropy, lse (rows,) float32, top_ids int32 and top_logp float32 (rows, k); what is None is not
     computed. Returns the status tensor."""
-    import torch
-    px, ld = _rows_of(logits, "logits", (torch.float32, torch.bfloat16))
-    rows = logits.shape[0]
-    if V > logits.shape[1]:
-        raise ValueError(f"V = {V} above the {logits.shape[1]} columns of logits")
+    torch = _torch or _import_torch()
+    f32, i32 = torch.float32, torch.int32
+    rows, cols, px, ld, code = _rows_of(logits, "logits", _FLOATS)
+    if V > cols:
+        raise ValueError(f"V = {V} above the {cols} columns of logits")
     k = 0 if top_ids is None else top_ids.shape[-1]
-    f32 = torch.float32
-    pt = _vector_of(targets, "targets", torch.int32, rows)
-    pl, pe, ps = (_vector_of(logp, "logp", f32, rows), _vector_of(entropy, "entropy", f32, rows),
-                  _vector_of(lse, "lse", f32, rows))
-    pi, pp = _vector_of(top_ids, "top_ids", torch.int32, rows * k), _vector_of(top_logp, "top_logp", f32, rows * k)
-    with _OnDevice((logits, targets, logp, entropy, lse, top_ids, top_logp), status, stream) as on:
-        _check(load_library().gpt2k_token_logprobs(_dtype_code(logits), px, rows, V, ld, temperature, pt, k, pl, pe,
-                                                   ps, pi, pp, _ptr(on.status), on.stream))
-    return on.status
+    pt, pl = _vector_of(targets, "targets", i32, rows), _vector_of(logp, "logp", f32, rows)
+    pe, ps = _vector_of(entropy, "entropy", f32, rows), _vector_of(lse, "lse", f32, rows)
+    pi, pp = _vector_of(top_ids, "top_ids", i32, rows * k), _vector_of(top_logp, "top_logp", f32, rows * k)
+    dev = _device_of(logits, targets, logp, entropy, lse, top_ids, top_logp, status)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    if status is None:
+        status = _status_on(dev, stream)
+    _call(dev, (_lib or load_library()).gpt2k_token_logprobs, code, px, rows, V, ld, temperature, pt, k, pl, pe, ps,
+          pi, pp, status.data_ptr(), stream)
+    return status
 
 
 def token_logprobs_bwd(logits, V: int, temperature: float, lse, dlogits, targets=None, dlogp=None, entropy=None,
                        dentropy=None, status=None, stream=None):
     """gpt2k_token_logprobs_bwd: dlogits (rows, >= V; the first V columns; logits' type, or logits itself) from
     dlogp and dentropy (rows,) float32 and the forward's lse and entropy. Returns the status tensor."""
-    import torch
-    px, ld = _rows_of(logits, "logits", (torch.float32, torch.bfloat16))
-    rows = logits.shape[0]
-    pd, ldd = _rows_of(dlogits, "dlogits", (logits.dtype,), rows)
-    if V > min(logits.shape[1], dlogits.shape[1]):
-        raise ValueError(f"V = {V} above the columns of logits or dlogits")
+    torch = _torch or _import_torch()
     f32 = torch.float32
+    rows, cols, px, ld, code = _rows_of(logits, "logits", _FLOATS)
+    _, dcols, pd, ldd, dcode = _rows_of(dlogits, "dlogits", _FLOATS, rows)
+    if V > cols or V > dcols:
+        raise ValueError(f"V = {V} above the columns of logits or dlogits")
+    if dcode != code:
+        raise ValueError("dlogits: the type of logits is needed")
     pt, pl = _vector_of(targets, "targets", torch.int32, rows), _vector_of(lse, "lse", f32, rows)
-    pg, pe, ph = (_vector_of(dlogp, "dlogp", f32, rows), _vector_of(entropy, "entropy", f32, rows),
-                  _vector_of(dentropy, "dentropy", f32, rows))
-    with _OnDevice((logits, lse, dlogits, targets, dlogp, entropy, dentropy), status, stream) as on:
-        _check(load_library().gpt2k_token_logprobs_bwd(_dtype_code(logits), px, rows, V, ld, temperature, pt, pl, pg,
-                                                       pe, ph, pd, ldd, _ptr(on.status), on.stream))
-    return on.status
+    pg, pe = _vector_of(dlogp, "dlogp", f32, rows), _vector_of(entropy, "entropy", f32, rows)
+    ph = _vector_of(dentropy, "dentropy", f32, rows)
+    dev = _device_of(logits, lse, dlogits, targets, dlogp, entropy, dentropy, status)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    if status is None:
+        status = _status_on(dev, stream)
+    _call(dev, (_lib or load_library()).gpt2k_token_logprobs_bwd, code, px, rows, V, ld, temperature, pt, pl, pg, pe,
+          ph, pd, ldd, status.data_ptr(), stream)
+    return status

@@ -229,8 +229,8 @@ int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scale, const in
  * lse, entropy, top_logp and a given target's logp; its ids are ordered with
  * NaN above every number. A target outside [-1, V) sets status bit 0 and is
  * clamped into [0, V). Errors: INVALID_ARG (unknown dtype, rows or V < 1,
- * ld < V, a temperature that is not finite and > 0 or whose reciprocal is
- * infinite, arguments that do not go together, a NULL or misaligned pointer). */
+ * ld < V, a temperature that is not finite and > 0 or below 4.5e-39 (1.5 /
+ * temperature infinite), arguments that do not go together, a NULL or misaligned pointer). */
 int gpt2k_token_logprobs(int dtype, const void* logits, int rows, int V, int64_t ld, float temperature,
                          const int32_t* targets, int top_k, float* logp, float* entropy, float* lse,
                          int32_t* top_ids, float* top_logp, uint32_t* status_dev, void* stream);
