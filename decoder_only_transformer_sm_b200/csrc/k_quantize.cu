@@ -5,10 +5,11 @@
 //
 // q is the nearest whole number (ties to even) of the exact quotient, so the
 // codes do not depend on how the quotient is rounded: t = x * fl32(127 / a)
-// is within 3 * 2^-24 * 127 < 2.3e-5 of it, and only a t closer than 3e-5 to the
+// is within 2 * 2^-24 * 127 < 1.6e-5 of it, and only a t closer than 3e-5 to the
 // border between two codes is decided by a 64-bit division (there 127 x is
 // exact, and a quotient that is not a border differs from one by more than
-// 2^-41 relative, so rounding the division cannot make a tie).
+// 2^-41 relative, so rounding the division cannot make a tie). So are rows whose
+// largest value is below 1e-30, where 127 / a could overflow.
 //
 // Bound by memory: a row is read once, as 16-byte vectors that stay in registers
 // (up to 8 a thread) between the maximum and the codes. Rows may start at
@@ -21,28 +22,47 @@ namespace gpt2 {
 
 namespace {
 
-struct RowScale {
-    float a;      // max |x|
-    float pre;    // power of two that keeps 127 / (a pre) finite
-    float inv;    // 127 / (a pre)
-};
+// t + MAGIC has the nearest whole number of t (ties to even, |t| < 2^22) in its low bits.
+constexpr float MAGIC = 12582912.f;   // 3 * 2^22
+constexpr float BORDER = 0.5f - 3e-5f;
 
-__device__ __forceinline__ RowScale row_scale(unsigned amax_bits) {
-    RowScale r;
-    r.a = __uint_as_float(amax_bits);
-    r.pre = r.a < 1e-30f ? 1.2676506e30f : 1.f;   // 2^100
-    r.inv = 127.f / (r.a * r.pre);
-    return r;
+__device__ __noinline__ unsigned code_at_border(float x, float a) {
+    return (unsigned)(int)rint(127.0 * (double)x / (double)a) & 0xffu;
 }
 
-__device__ __noinline__ int code_at_border(float x, float a) { return (int)rint(127.0 * (double)x / (double)a); }
-
-__device__ __forceinline__ int code(float x, const RowScale& r) {
-    const float t = (x * r.pre) * r.inv;
-    const float n = rintf(t);
-    if (fabsf(fabsf(t - n) - 0.5f) < 3e-5f) return code_at_border(x, r.a);
-    return (int)n;
+// Codes of N values as N bytes: inv = 127 / a, 0 where that is no normal number (every
+// code is then taken from the 64-bit quotient; a = 0 gives 0).
+template <int N>
+__device__ __forceinline__ void codes(const float (&x)[N], float a, float inv, unsigned (&out)[N / 4]) {
+    unsigned c[N];
+    float far = 0.f;
+    const f32x2 i2 = pk2(inv, inv), up = pk2(MAGIC, MAGIC), down = pk2(-MAGIC, -MAGIC), minus = pk2(-1.f, -1.f);
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+        const f32x2 t = mul2(pk2(x[j], x[j + 1]), i2);
+        const f32x2 n = add2(t, up);
+        float n0, n1, f0, f1;
+        upk2(n, n0, n1);
+        upk2(fma2(add2(n, down), minus, t), f0, f1);
+        far = fmaxf(far, fmaxf(fabsf(f0), fabsf(f1)));
+        c[j] = __float_as_uint(n0);
+        c[j + 1] = __float_as_uint(n1);
+    }
+    if (far > BORDER || inv == 0.f) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) c[j] = a > 0.f ? code_at_border(x[j], a) : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < N; j += 4)
+        out[j / 4] = __byte_perm(__byte_perm(c[j], c[j + 1], 0x0040), __byte_perm(c[j + 2], c[j + 3], 0x0040), 0x5410);
 }
+__device__ __forceinline__ unsigned code(float x, float a, float inv) {
+    const float t = x * inv, n = t + MAGIC;
+    if (fabsf(t - (n - MAGIC)) > BORDER || inv == 0.f) return a > 0.f ? code_at_border(x, a) : 0u;
+    return __float_as_uint(n) & 0xffu;
+}
+// 127 / a, or 0 where a is so small (or no number) that the 64-bit quotient is taken.
+__device__ __forceinline__ float inverse(float a) { return a > 1e-30f ? 127.f / a : 0.f; }
 
 // The bits of |x| order like its value, with inf and NaN above every finite one.
 __device__ __forceinline__ unsigned magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
@@ -65,17 +85,35 @@ __global__ void __launch_bounds__(256) quantize_long_rows_kernel(const T* __rest
     for (int w = 1; w < 8; ++w) m = max(m, part[w]);
     const bool fine = m < 0x7f800000u;
     if (threadIdx.x == 0) scale[blockIdx.x] = fine ? __uint_as_float(m) / 127.f : __uint_as_float(0x7fc00000u);
-    const RowScale r = row_scale(m);
-    for (int k = threadIdx.x; k < K; k += 256) qr[k] = fine && m ? (int8_t)code(to_f(xr[k]), r) : (int8_t)0;
+    const float a = fine ? __uint_as_float(m) : 0.f, inv = inverse(a);
+    for (int k = threadIdx.x; k < K; k += 256) qr[k] = (int8_t)code(to_f(xr[k]), a, inv);
 }
 
-__device__ __forceinline__ float element(const uint4& q, int j, float) {
-    return __uint_as_float(j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w);
+__device__ __forceinline__ void unpack(const uint4& q, float (&f)[8], bf16) {
+    const unsigned u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
 }
-__device__ __forceinline__ float element(const uint4& q, int j, bf16) {
-    const unsigned w = j < 2 ? q.x : j < 4 ? q.y : j < 6 ? q.z : q.w;
-    return __uint_as_float((j & 1) ? w & 0xffff0000u : w << 16);
+__device__ __forceinline__ void unpack(const uint4& q, float (&f)[4], float) {
+    f[0] = __uint_as_float(q.x);
+    f[1] = __uint_as_float(q.y);
+    f[2] = __uint_as_float(q.z);
+    f[3] = __uint_as_float(q.w);
 }
+// Largest magnitude of a vector: two 16-bit ones at a time for bf16 (`m` in both halves).
+__device__ __forceinline__ unsigned larger(unsigned m, const uint4& q, bf16) {
+    constexpr unsigned K2 = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(m, __vmaxu2(q.x & K2, q.y & K2)), __vmaxu2(q.z & K2, q.w & K2));
+}
+__device__ __forceinline__ unsigned larger(unsigned m, const uint4& q, float) {
+    constexpr unsigned K1 = 0x7fffffffu;
+    return max(max(m, max(q.x & K1, q.y & K1)), max(q.z & K1, q.w & K1));
+}
+__device__ __forceinline__ unsigned whole(unsigned m, bf16) { return max(m << 16, m & 0xffff0000u); }
+__device__ __forceinline__ unsigned whole(unsigned m, float) { return m; }
 
 constexpr int QT = 256, QV = 8;   // threads a block, vectors a thread
 
@@ -104,11 +142,9 @@ __global__ void __launch_bounds__(QT) quantize_rows_kernel(const T* __restrict__
             v[i] = t + i * G < full ? __ldg(reinterpret_cast<const uint4*>(xr + head) + t + i * G) : make_uint4(0, 0, 0, 0);
         if (t < head) h = to_f(xr[t]);
         if (t < tail) e = to_f(xr[K - tail + t]);
-        m = max(magnitude(h), magnitude(e));
 #pragma unroll
-        for (int i = 0; i < QV; ++i)
-#pragma unroll
-            for (int j = 0; j < N; ++j) m = max(m, magnitude(element(v[i], j, T())));
+        for (int i = 0; i < QV; ++i) m = larger(m, v[i], T());
+        m = max(whole(m, T()), max(magnitude(h), magnitude(e)));
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (G > 32) {
@@ -120,29 +156,29 @@ __global__ void __launch_bounds__(QT) quantize_rows_kernel(const T* __restrict__
     }
     const bool fine = m < 0x7f800000u;
     if (live && t == 0) scale[row] = fine ? __uint_as_float(m) / 127.f : __uint_as_float(0x7fc00000u);
-    const RowScale r = row_scale(fine && m ? m : 0x3f800000u);
-    const bool zero = !fine;   // (a row of zeros has codes 0 by any scale)
+    const float a = fine ? __uint_as_float(m) : 0.f, inv = inverse(a);
     const int lead = (int)((uintptr_t)qr & 15);
     int8_t* room = reinterpret_cast<int8_t*>(staged) + in_block * ((K + 15 + 16 + 15) / 16 * 16) + lead;
     if (live) {
-        if (t < head) room[t] = zero ? 0 : code(h, r);
-        if (t < tail) room[K - tail + t] = zero ? 0 : code(e, r);
+        if (t < head) room[t] = (int8_t)code(h, a, inv);
+        if (t < tail) room[K - tail + t] = (int8_t)code(e, a, inv);
         const bool words = ((lead + head) & 3) == 0;
 #pragma unroll
         for (int i = 0; i < QV; ++i) {
             if (t + i * G < full) {
-                int c[N];
-#pragma unroll
-                for (int j = 0; j < N; ++j) c[j] = zero ? 0 : code(element(v[i], j, T()), r);
+                float f[N];
+                unsigned c[N / 4];
+                unpack(v[i], f, T());
+                codes<N>(f, a, inv, c);
                 int8_t* at = room + head + (t + i * G) * N;
-                if (words) {
 #pragma unroll
-                    for (int j = 0; j < N; j += 4)
-                        *reinterpret_cast<unsigned*>(at + j) = (c[j] & 0xff) | (c[j + 1] & 0xff) << 8 |
-                                                               (c[j + 2] & 0xff) << 16 | (unsigned)c[j + 3] << 24;
-                } else {
+                for (int j = 0; j < N / 4; ++j) {
+                    if (words) {
+                        reinterpret_cast<unsigned*>(at)[j] = c[j];
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < N; ++j) at[j] = (int8_t)c[j];
+                        for (int b = 0; b < 4; ++b) at[4 * j + b] = (int8_t)(c[j] >> (8 * b));
+                    }
                 }
             }
         }

@@ -12,11 +12,13 @@
 // Forward: one pass over the row. A thread keeps a running (m, s, w) and rescales
 // it when a load of several vectors raises m; the block's threads, and with few rows
 // the blocks of a cluster (distributed shared memory), join theirs at the end.
-// Top alternatives come from the same pass: four neighbouring lanes share a group,
+// Top alternatives come from the same pass: four neighbouring threads share a group,
 // whose largest value is known at the end. A group is read again (from L2) only if
 // fewer than top_k groups have a larger maximum: no other group can hold one of the
-// top_k, and their smallest maximum is a bound that few other values pass. What passes it is
-// merged in sorted lists of 64-bit keys (value, then lowest index), one list a warp.
+// top_k, and the smallest maximum of those read again is a bound that few other values
+// pass. What passes it is ranked by 64-bit keys (value, then lowest index). Where more
+// values pass than there is room for (many equal ones), each warp instead keeps a sorted list while it
+// reads its own groups again.
 #include <cooperative_groups.h>
 
 #include "kernels.cuh"
@@ -76,25 +78,86 @@ __device__ __forceinline__ void unpack(const uint4& q, float (&f)[4], float) {
     f[3] = __uint_as_float(q.w);
 }
 
-// Vector i's bits; what lies outside the row (and a vector past the end) is -inf.
+__device__ __forceinline__ uint4 pack(const float (&f)[8], bf16) {
+    uint4 q;
+    unsigned* u = reinterpret_cast<unsigned*>(&q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        u[i] = *reinterpret_cast<const unsigned*>(&t);
+    }
+    return q;
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[4], float) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+
+// Vector i element by element: for the ends of a row, and for rows whose vectors are laid out
+// after another row's boundaries. What lies outside is -inf.
 template <typename T>
-__device__ __forceinline__ uint4 load_vec(const T* row, const RowVecs<T>& rv, int i, int end) {
+__device__ __noinline__ uint4 gather_vec(const T* row, const RowVecs<T> rv, int i, int end) {
     constexpr unsigned NONE = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-    uint4 q = make_uint4(NONE, NONE, NONE, NONE);
+    union {
+        uint4 q;
+        T t[RowVecs<T>::N];
+    } u;
+    u.q = make_uint4(NONE, NONE, NONE, NONE);
     if (i < end) {
-        if (rv.whole(i)) return __ldg(reinterpret_cast<const uint4*>(row + rv.head) + (i - 1));
-        union {
-            uint4 q;
-            T t[RowVecs<T>::N];
-        } u;
-        u.q = q;
         const int a = rv.first(i), b = rv.last(i);
 #pragma unroll
         for (int j = 0; j < RowVecs<T>::N; ++j)
             if (a + j < b) u.t[j] = row[a + j];
-        q = u.q;
     }
-    return q;
+    return u.q;
+}
+template <typename T>
+__device__ __noinline__ void scatter_vec(T* row, const RowVecs<T> rv, int i, uint4 q) {
+    union {
+        uint4 q;
+        T t[RowVecs<T>::N];
+    } u;
+    u.q = q;
+    const int a = rv.first(i), b = rv.last(i);
+#pragma unroll
+    for (int j = 0; j < RowVecs<T>::N; ++j)
+        if (a + j < b) row[a + j] = u.t[j];
+}
+
+// Vector i's bits; what lies outside the row (and a vector past the end) is -inf.
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const T* row, const RowVecs<T>& rv, int i, int end) {
+    if (i < end && rv.whole(i)) return __ldg(reinterpret_cast<const uint4*>(row + rv.head) + (i - 1));
+    return gather_vec(row, rv, i, end);
+}
+
+// Largest and smallest of U vectors, NaN passed over.
+template <int U>
+__device__ __forceinline__ void extremes(const uint4 (&q)[U], float& top, float& low, bf16) {
+    __nv_bfloat162 hi, lo;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q[u]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            hi = u + j ? __hmax2(hi, h[j]) : h[j];
+            lo = u + j ? __hmin2(lo, h[j]) : h[j];
+        }
+    }
+    const float2 a = __bfloat1622float2(hi), b = __bfloat1622float2(lo);
+    top = fmaxf(a.x, a.y);
+    low = fminf(b.x, b.y);
+}
+template <int U>
+__device__ __forceinline__ void extremes(const uint4 (&q)[U], float& top, float& low, float) {
+    top = NEG_INF;
+    low = -NEG_INF;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float f[4];
+        unpack(q[u], f, 0.f);
+        top = fmaxf(fmaxf(top, fmaxf(f[0], f[1])), fmaxf(f[2], f[3]));
+        low = fminf(fminf(low, fminf(f[0], f[1])), fminf(f[2], f[3]));
+    }
 }
 
 struct Sums {
@@ -111,6 +174,37 @@ struct Sums {
         o.raise(to, c);
         s += o.s;
         w += o.w;
+    }
+    // The terms of U vectors, none above m. MASKED: there may be -inf, whose e = 0 meets d = -inf.
+    template <bool MASKED, typename T, int U>
+    __device__ __forceinline__ void add(const uint4 (&q)[U], float c) {
+        constexpr int N = RowVecs<T>::N;
+        const f32x2 m2 = pk2(-m, -m), c2 = pk2(c, c);
+        f32x2 s2 = pk2(s, 0.f), w2 = pk2(w, 0.f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float f[N];
+            unpack(q[u], f, T());
+#pragma unroll
+            for (int j = 0; j < N; j += 2) {
+                f32x2 d2 = add2(pk2(f[j], f[j + 1]), m2);
+                float y0, y1;
+                upk2(mul2(d2, c2), y0, y1);
+                const f32x2 e2 = pk2(ex2_approx(y0), ex2_approx(y1));
+                if (MASKED) {
+                    float d0, d1;
+                    upk2(d2, d0, d1);
+                    d2 = pk2(fmaxf(d0, -3.402823466e38f), fmaxf(d1, -3.402823466e38f));
+                }
+                s2 = add2(s2, e2);
+                w2 = fma2(e2, d2, w2);
+            }
+        }
+        float s0, s1, w0, w1;
+        upk2(s2, s0, s1);
+        upk2(w2, w0, w1);
+        s = s0 + s1;
+        w = w0 + w1;
     }
     __device__ __forceinline__ Sums shuffled(int mask) const {
         return {__shfl_xor_sync(0xffffffffu, m, mask), __shfl_xor_sync(0xffffffffu, s, mask),
@@ -136,8 +230,9 @@ struct ForwardSmem {
     alignas(16) unsigned group[NT / 4];   // order of each group's largest value
     u64 cand[NT];                         // the warps' lists, packed
     Sums sums[NT / 32];
+    int again[NT / 4];                    // first threads of the groups to read again
     unsigned bound;
-    int n_cand;
+    int n_cand, n_again;
     // of the cluster's first block: every block's results
     Sums all_sums[8];
     u64 all_top[8 * LOGPROB_MAX_TOP];
@@ -155,11 +250,112 @@ __device__ __forceinline__ void for_top(const u64* keys, int n, int k, int nt, F
     }
 }
 
+// Leaves in sm.cand (sm.n_cand of them, visible to the block) keys among which are the
+// block's top_k. order: the largest of the thread's group, as in sm.group.
+template <typename T, int NT>
+__device__ __forceinline__ void top_of_block(ForwardSmem<NT>& sm, const T* x, const RowVecs<T>& rv, int begin, int end,
+                                             unsigned order, int top_k) {
+    constexpr int N = RowVecs<T>::N;
+    const int tid = threadIdx.x, lane = tid & 31;
+    int above = 0;
+#pragma unroll
+    for (int j = 0; j < NT / 4; j += 4) {
+        const uint4 g = *reinterpret_cast<const uint4*>(sm.group + j);
+        above += (g.x > order) + (g.y > order) + (g.z > order) + (g.w > order);
+    }
+    const bool again = above < top_k;
+    if (again && (tid & 3) == 0) {
+        atomicMin(&sm.bound, order);
+        sm.again[atomicAdd(&sm.n_again, 1)] = tid;
+    }
+    __syncthreads();
+    const unsigned bound = sm.bound;
+    const float bound_value = value_of(bound);
+    const int steps = ceil_div(end - begin, NT), n_again = sm.n_again;
+    if (n_again <= 2 * top_k) {
+        // a thread takes single vectors of all the groups
+        constexpr int R = 4;
+        for (int k0 = tid; k0 < n_again * steps * 4; k0 += R * NT) {
+            uint4 q[R];
+            int at[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int k = k0 + r * NT, g = k / (4 * steps);
+                at[r] = g < n_again ? begin + (k % (4 * steps)) / 4 * NT + sm.again[g] + (k & 3) : end;
+                q[r] = load_vec(x, rv, at[r], end);
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (at[r] >= end) continue;
+                float f[N];
+                unpack(q[r], f, T());
+                bool pass = false;
+#pragma unroll
+                for (int j = 0; j < N; ++j) pass |= !(f[j] < bound_value);
+                if (!pass) continue;
+                const int first = rv.first(at[r]), last = rv.last(at[r]);
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const unsigned o = order_of(f[j]);
+                    if (o >= bound && first + j < last) {
+                        const int n = atomicAdd(&sm.n_cand, 1);
+                        if (n < NT) sm.cand[n] = key_of(o, first + j);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (sm.n_cand <= NT) return;
+        __syncthreads();
+        if (tid == 0) sm.n_cand = 0;
+        __syncthreads();
+    }
+    u64 list = 0;
+    // 32 lanes read a group's four vectors (one step of the pass), or two steps' of them
+    constexpr int STEPS = 32 / (4 * N);
+    for (unsigned todo = __ballot_sync(0xffffffffu, again && (tid & 3) == 0); todo; todo &= todo - 1) {
+        const int g0 = (tid & ~31) + __ffs(todo) - 1;
+        const int mine = g0 + (lane / N) % 4, j = lane % N;
+        constexpr int R = 8;
+        for (int i0 = begin; i0 < end; i0 += R * STEPS * NT) {
+            float v[R];
+            int at[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int i = i0 + (r * STEPS + lane / (4 * N)) * NT + mine;
+                at[r] = -1;
+                v[r] = 0.f;
+                if (i < end) {
+                    const int e = rv.first(i) + j;
+                    if (e < rv.last(i)) {
+                        at[r] = e;
+                        v[r] = to_f(x[e]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const unsigned o = order_of(v[r]);
+                const u64 k = key_of(o, at[r]);
+                // at most top_k of the list can be among the row's
+                const u64 least = __shfl_sync(0xffffffffu, list, top_k - 1);
+                insert(list, k, at[r] >= 0 && o >= bound && k > least);
+            }
+        }
+    }
+    const unsigned kept = __ballot_sync(0xffffffffu, list != 0 && lane < top_k);
+    int base = 0;
+    if (lane == 0 && kept) base = atomicAdd(&sm.n_cand, __popc(kept));
+    base = __shfl_sync(0xffffffffu, base, 0);
+    if ((kept >> lane) & 1) sm.cand[base + __popc(kept & ((1u << lane) - 1))] = list;
+    __syncthreads();
+}
+
 template <typename T, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(NT) token_logprobs_kernel(const T* __restrict__ logits, long long ld, int V,
                                                             float inv_tau, const int* __restrict__ targets,
                                                             LogprobOut out, int parts, unsigned* status) {
-    constexpr int N = RowVecs<T>::N, U = 4;
+    constexpr int U = 4;
     __shared__ ForwardSmem<NT> sm;
     const int tid = threadIdx.x, lane = tid & 31;
     const int row = CLUSTER ? blockIdx.x / parts : blockIdx.x, part = CLUSTER ? blockIdx.x % parts : 0;
@@ -171,51 +367,32 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const T* __restrict_
     if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     if (tid == 0) {
         sm.bound = 0xffffffffu;
-        sm.n_cand = 0;
+        sm.n_cand = sm.n_again = 0;
     }
 
     Sums a = {-3.402823466e38f, 0.f, 0.f};
     float largest = NEG_INF;
     for (int i = begin + tid; i < end; i += U * NT) {
         uint4 q[U];
+        if (i > 0 && i + (U - 1) * NT < min(end, rv.full + 1)) {
+            const uint4* at = reinterpret_cast<const uint4*>(x + rv.head) + (i - 1);
 #pragma unroll
-        for (int u = 0; u < U; ++u) q[u] = load_vec(x, rv, i + u * NT, end);
-        float f[U][N];
-        float top = NEG_INF;
+            for (int u = 0; u < U; ++u) q[u] = __ldg(at + u * NT);
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            unpack(q[u], f[u], T());
-#pragma unroll
-            for (int j = 0; j < N; ++j) top = fmaxf(top, f[u][j]);
+            for (int u = 0; u < U; ++u) q[u] = load_vec(x, rv, i + u * NT, end);
         }
+        float top, low;
+        extremes(q, top, low, T());
         largest = fmaxf(largest, top);
         if (top > a.m) a.raise(top, c);
-        const f32x2 m2 = pk2(-a.m, -a.m), c2 = pk2(c, c);
-        f32x2 s2 = pk2(a.s, 0.f), w2 = pk2(a.w, 0.f);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int j = 0; j < N; j += 2) {
-                const f32x2 d2 = add2(pk2(f[u][j], f[u][j + 1]), m2);
-                float y0, y1, d0, d1;
-                upk2(mul2(d2, c2), y0, y1);
-                upk2(d2, d0, d1);
-                const f32x2 e2 = pk2(ex2_approx(y0), ex2_approx(y1));
-                s2 = add2(s2, e2);
-                // a masked value has e = 0 and d = -inf
-                w2 = fma2(e2, pk2(fmaxf(d0, -1e30f), fmaxf(d1, -1e30f)), w2);
-            }
-        }
-        float s0, s1, w0, w1;
-        upk2(s2, s0, s1);
-        upk2(w2, w0, w1);
-        a.s = s0 + s1;
-        a.w = w0 + w1;
+        if (low > -1e30f) a.add<false, T>(q, c);
+        else a.add<true, T>(q, c);
     }
 
+    unsigned order = 0;   // of this thread's largest value, then of its group's
     if (out.top_k) {
-        unsigned order = largest == NEG_INF ? 0u : order_of(largest);
-        if (largest == NEG_INF && begin + tid < end) order = order_of(NEG_INF);
+        if (begin + tid < end) order = order_of(largest);
         if (a.s != a.s) {   // a NaN, or +inf: find out which
             for (int i = begin + tid; i < end; i += NT)
                 for (int v = rv.first(i); v < rv.last(i); ++v) order = max(order, order_of(to_f(x[v])));
@@ -223,57 +400,7 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const T* __restrict_
         order = max(order, __shfl_xor_sync(0xffffffffu, order, 1));
         order = max(order, __shfl_xor_sync(0xffffffffu, order, 2));
         if ((tid & 3) == 0) sm.group[tid >> 2] = order;
-        __syncthreads();
-        int above = 0;
-#pragma unroll
-        for (int j = 0; j < NT / 4; j += 4) {
-            const uint4 g = *reinterpret_cast<const uint4*>(sm.group + j);
-            above += (g.x > order) + (g.y > order) + (g.z > order) + (g.w > order);
-        }
-        const bool again = above < out.top_k;
-        if (again && (tid & 3) == 0) atomicMin(&sm.bound, order);
-        __syncthreads();
-        const unsigned bound = sm.bound;
-        u64 list = 0;
-        // 32 lanes read a group's four vectors (one step of the pass), or two steps' of them
-        constexpr int STEPS = 32 / (4 * N);
-        for (unsigned todo = __ballot_sync(0xffffffffu, again && (tid & 3) == 0); todo; todo &= todo - 1) {
-            const int g0 = (tid & ~31) + __ffs(todo) - 1;
-            const int mine = g0 + (lane / N) % 4, j = lane % N;
-            constexpr int R = 8;
-            for (int i0 = begin; i0 < end; i0 += R * STEPS * NT) {
-                float v[R];
-                int at[R];
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int i = i0 + (r * STEPS + lane / (4 * N)) * NT + mine;
-                    at[r] = -1;
-                    v[r] = 0.f;
-                    if (i < end) {
-                        const int e = rv.first(i) + j;
-                        if (e < rv.last(i)) {
-                            at[r] = e;
-                            v[r] = to_f(x[e]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const unsigned o = order_of(v[r]);
-                    const u64 k = key_of(o, at[r]);
-                    // at most top_k of the list can be among the row's
-                    const u64 least = __shfl_sync(0xffffffffu, list, out.top_k - 1);
-                    insert(list, k, at[r] >= 0 && o >= bound && k > least);
-                }
-            }
-        }
-        const unsigned kept = __ballot_sync(0xffffffffu, list != 0 && lane < out.top_k);
-        int base = 0;
-        if (lane == 0 && kept) base = atomicAdd(&sm.n_cand, __popc(kept));
-        base = __shfl_sync(0xffffffffu, base, 0);
-        if ((kept >> lane) & 1) sm.cand[base + __popc(kept & ((1u << lane) - 1))] = list;
     }
-    __syncwarp();
 #pragma unroll
     for (int o = 16; o; o >>= 1) a.join(a.shuffled(o), c);
     if (lane == 0) sm.sums[tid >> 5] = a;
@@ -281,8 +408,9 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const T* __restrict_
     a = sm.sums[0];
 #pragma unroll
     for (int w = 1; w < NT / 32; ++w) a.join(sm.sums[w], c);
+    if (out.top_k && (CLUSTER || a.s != 0.f)) top_of_block<T, NT>(sm, x, rv, begin, end, order, out.top_k);
     const u64* keys = sm.cand;
-    int n_keys = out.top_k ? sm.n_cand : 0;
+    int n_keys = sm.n_cand;
     if (CLUSTER) {
         auto cluster = cg::this_cluster();
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // every block has started
@@ -316,7 +444,11 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const T* __restrict_
             out.logp[row] = t < 0 ? 0.f : logp_of(to_f(x[t]));
         }
     }
-    for_top(keys, n_keys, out.top_k, NT, [&](int r, u64 k) {
+    if (a.s == 0.f && tid < out.top_k) {   // every logit is -inf
+        out.top_ids[(long long)row * out.top_k + tid] = tid;
+        out.top_logp[(long long)row * out.top_k + tid] = NEG_INF;
+    }
+    if (a.s != 0.f) for_top(keys, n_keys, out.top_k, NT, [&](int r, u64 k) {
         out.top_ids[(long long)row * out.top_k + r] = (int)~(unsigned)k;
         out.top_logp[(long long)row * out.top_k + r] = logp_of(value_of((unsigned)(k >> 32)));
     });
@@ -349,56 +481,51 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, lo
     const bool none = (g == 0.f && h == 0.f) || L == NEG_INF;
     const float gt = g * inv_tau, A = -(g + h * H) * inv_tau, B = -h * inv_tau;
     const RowVecs<T> rv(dx, V);   // the vectors of what is written
-    const bool same = (((uintptr_t)x ^ (uintptr_t)dx) & 15) == 0;
     const int per = ceil_div(rv.count(), parts), end = min(rv.count(), (part + 1) * per);
-    for (int i = part * per + threadIdx.x; i < end; i += U * 256) {
-        union V16 {
-            uint4 q;
-            T t[N];
-            __device__ V16() {}
-        } v[U];
-        if (!none) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int k = i + u * 256;
-                if (k < end && rv.whole(k) && same) {
-                    v[u].q = *(reinterpret_cast<const uint4*>(x + rv.head) + (k - 1));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < N; ++j) v[u].t[j] = k < end && rv.first(k) + j < rv.last(k) ? x[rv.first(k) + j] : from_f<T>(0.f);
-                }
-            }
-        }
+    const int i0 = part * per + threadIdx.x;
+    const bool same = (((uintptr_t)x ^ (uintptr_t)dx) & 15) == 0;
+    // a thread's vectors i0, i0 + 256, ..: at most U of them (`parts`)
+    uint4 q[U];
+    if (!none) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = i + u * 256;
-            if (k >= end) break;
-            const int first = rv.first(k);
-            if (none) {
-                v[u].q = make_uint4(0, 0, 0, 0);
-            } else {
-                float r[N];
+            const int k = i0 + u * 256;
+            if (k < end && rv.whole(k) && same) q[u] = *(reinterpret_cast<const uint4*>(x + rv.head) + (k - 1));
+            else q[u] = gather_vec(x, rv, k, end);
+        }
+    }
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const float d = fmaf(to_f(v[u].t[j]), inv_tau, -L);
-                    const float p = ex2_approx(d * LOG2E);
-                    r[j] = p * fmaf(B, fmaxf(d, -1e30f), A);   // a masked value: p = 0, d = -inf
-                }
-                if ((unsigned)(t - first) < (unsigned)N) {
+    for (int u = 0; u < U; ++u) {
+        const int k = i0 + u * 256;
+        if (k >= end) break;
+        const int first = rv.first(k);
+        if (none) {
+            q[u] = make_uint4(0, 0, 0, 0);
+        } else {
+            float r[N];
+            unpack(q[u], r, T());
+            const f32x2 it2 = pk2(inv_tau, inv_tau), l2 = pk2(-L, -L), e2 = pk2(LOG2E, LOG2E), A2 = pk2(A, A), B2 = pk2(B, B);
 #pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        if (first + j == t) r[j] += gt;
-                }
-#pragma unroll
-                for (int j = 0; j < N; ++j) v[u].t[j] = from_f<T>(r[j]);
+            for (int j = 0; j < N; j += 2) {
+                const f32x2 d2 = fma2(pk2(r[j], r[j + 1]), it2, l2);
+                float d0, d1, y0, y1;
+                upk2(d2, d0, d1);
+                upk2(mul2(d2, e2), y0, y1);
+                // a masked value: p = 0, d = -inf
+                const f32x2 f2 = fma2(B2, pk2(fmaxf(d0, -1e30f), fmaxf(d1, -1e30f)), A2);
+                upk2(mul2(pk2(ex2_approx(y0), ex2_approx(y1)), f2), r[j], r[j + 1]);
             }
-            if (rv.whole(k)) {
-                *(reinterpret_cast<uint4*>(dx + rv.head) + (k - 1)) = v[u].q;
-            } else {
+            if ((unsigned)(t - first) < (unsigned)N) {
 #pragma unroll
                 for (int j = 0; j < N; ++j)
-                    if (first + j < rv.last(k)) dx[first + j] = v[u].t[j];
+                    if (first + j == t) r[j] += gt;
             }
+            q[u] = pack(r, T());
+        }
+        if (rv.whole(k)) {
+            *(reinterpret_cast<uint4*>(dx + rv.head) + (k - 1)) = q[u];
+        } else {
+            scatter_vec(dx, rv, k, q[u]);
         }
     }
 }

@@ -86,17 +86,19 @@ def test_binding_refusals():
 
 
 def test_fp32_quotient_is_within_its_bound():
-    """The kernel takes the code of fl(fl(x pre) fl(127 / (a pre))) unless it lies within 3e-5 of a border, and
-    decides those by a 64-bit division: the fp32 value has to be within 3e-5 of the quotient (three roundings of half
-    a step each, 127 * 3 * 2^-24 = 2.3e-5), and the quotient's 64-bit rounding must not make or lose a tie."""
+    """For a > 1e-30 the kernel takes the code of t = fl(x fl(127 / a)), read from the low bits of fl(t + 3 2^22), unless
+    t lies within 3e-5 of a border, and decides those (and smaller a) by a 64-bit division: t has to be within 3e-5 of
+    the quotient (two roundings of half a step each, 127 * 2 * 2^-24 = 1.6e-5), and the quotient's 64-bit rounding
+    must not make or lose a tie."""
     rng = np.random.default_rng(0)
-    for scale in (1.0, 1e-42, 1e-30, 3e37):
+    for scale in (1.0, 1e-26, 3e37):
         a = (np.abs(rng.standard_normal(200000)) * scale + scale * 1e-3).astype(np.float32)
         x = (a * rng.uniform(-1, 1, a.size)).astype(np.float32)
-        pre = np.where(a < np.float32(1e-30), np.float32(2.0 ** 100), np.float32(1.0))
-        t = (x * pre) * (np.float32(127.0) / (a * pre))
+        t = x * (np.float32(127.0) / a)
         exact = 127.0 * x.astype(np.float64) / a.astype(np.float64)
-        assert np.max(np.abs(t.astype(np.float64) - exact)) < 3e-5
+        assert np.max(np.abs(t.astype(np.float64) - exact)) < 1.6e-5
+        whole = (t + np.float32(12582912.0)).view(np.uint32) & 0xff
+        assert np.array_equal(whole.astype(np.uint8).view(np.int8), np.rint(t).astype(np.int8))
     # ties: a = 254 2^e, x = odd 2^e give quotients (2 k + 1) / 2; their fp32 neighbours do not
     for e in (-120, 0, 100):
         a = np.float32(254.0 * 2.0 ** e)
