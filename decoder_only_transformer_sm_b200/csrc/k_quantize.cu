@@ -5,7 +5,7 @@
 //
 // q is the nearest whole number (ties to even) of the exact quotient, so the
 // codes do not depend on how the quotient is rounded: t = x * fl32(127 / a)
-// is within 2 * 2^-24 * 127 < 1.6e-5 of it, and only a t closer than 3e-5 to the
+// is within 2 * 2^-24 * 127 < 1.6e-5 of it, and only a t closer than 1.7e-5 to the
 // border between two codes is decided by a 64-bit division (there 127 x is
 // exact, and a quotient that is not a border differs from one by more than
 // 2^-41 relative, so rounding the division cannot make a tie). So are rows whose
@@ -24,7 +24,7 @@ namespace {
 
 // t + MAGIC has the nearest whole number of t (ties to even, |t| < 2^22) in its low bits.
 constexpr float MAGIC = 12582912.f;   // 3 * 2^22
-constexpr float BORDER = 0.5f - 3e-5f;
+constexpr float BORDER = 0.5f - 1.7e-5f;
 
 __device__ __noinline__ unsigned code_at_border(float x, float a) {
     return (unsigned)(int)rint(127.0 * (double)x / (double)a) & 0xffu;
@@ -35,22 +35,23 @@ __device__ __noinline__ unsigned code_at_border(float x, float a) {
 template <int N>
 __device__ __forceinline__ void codes(const float (&x)[N], float a, float inv, unsigned (&out)[N / 4]) {
     unsigned c[N];
-    float far = 0.f;
+    float off[N], far = 0.f;
     const f32x2 i2 = pk2(inv, inv), up = pk2(MAGIC, MAGIC), down = pk2(-MAGIC, -MAGIC), minus = pk2(-1.f, -1.f);
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
         const f32x2 t = mul2(pk2(x[j], x[j + 1]), i2);
         const f32x2 n = add2(t, up);
-        float n0, n1, f0, f1;
+        float n0, n1;
         upk2(n, n0, n1);
-        upk2(fma2(add2(n, down), minus, t), f0, f1);
-        far = fmaxf(far, fmaxf(fabsf(f0), fabsf(f1)));
+        upk2(fma2(add2(n, down), minus, t), off[j], off[j + 1]);
+        far = fmaxf(far, fmaxf(fabsf(off[j]), fabsf(off[j + 1])));
         c[j] = __float_as_uint(n0);
         c[j + 1] = __float_as_uint(n1);
     }
     if (far > BORDER || inv == 0.f) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) c[j] = a > 0.f ? code_at_border(x[j], a) : 0u;
+        for (int j = 0; j < N; ++j)
+            if (fabsf(off[j]) > BORDER || inv == 0.f) c[j] = a > 0.f ? code_at_border(x[j], a) : 0u;
     }
 #pragma unroll
     for (int j = 0; j < N; j += 4)
@@ -115,11 +116,11 @@ __device__ __forceinline__ unsigned larger(unsigned m, const uint4& q, float) {
 __device__ __forceinline__ unsigned whole(unsigned m, bf16) { return max(m << 16, m & 0xffff0000u); }
 __device__ __forceinline__ unsigned whole(unsigned m, float) { return m; }
 
-constexpr int QT = 256, QV = 8;   // threads a block, vectors a thread
+constexpr int QV = 8;   // vectors a thread
 
-// G threads a row, QT / G rows a block.
-template <typename T, int G>
-__global__ void __launch_bounds__(QT) quantize_rows_kernel(const T* __restrict__ x, long long ldx, int rows, int K,
+// G threads a row, QT a block.
+template <typename T, int G, int QT>
+__global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* __restrict__ x, long long ldx, int rows, int K,
                                                            int8_t* __restrict__ q, long long ldq,
                                                            float* __restrict__ scale) {
     constexpr int N = 16 / sizeof(T);
@@ -195,10 +196,10 @@ __global__ void __launch_bounds__(QT) quantize_rows_kernel(const T* __restrict__
     }
 }
 
-template <typename T, int G>
+template <typename T, int G, int QT = (G > 128 ? G : 128)>
 void launch_short(const Ctx& ctx, const T* x, long long ldx, int rows, int K, int8_t* q, long long ldq, float* scale) {
     const size_t room = (size_t)(QT / G) * ((K + 15 + 16 + 15) / 16 * 16);
-    quantize_rows_kernel<T, G><<<ceil_div(rows, QT / G), QT, room, ctx.stream>>>(x, ldx, rows, K, q, ldq, scale);
+    quantize_rows_kernel<T, G, QT><<<ceil_div(rows, QT / G), QT, room, ctx.stream>>>(x, ldx, rows, K, q, ldq, scale);
 }
 
 }  // namespace

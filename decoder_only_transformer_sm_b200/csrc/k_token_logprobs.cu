@@ -12,7 +12,7 @@
 // Forward: one pass over the row. A thread keeps a running (m, s, w) and rescales
 // it when a load of several vectors raises m; the block's threads, and with few rows
 // the blocks of a cluster (distributed shared memory), join theirs at the end.
-// Top alternatives come from the same pass: four neighbouring threads share a group,
+// Top alternatives come from the same pass: neighbouring threads share one of 64 groups,
 // whose largest value is known at the end. A group is read again (from L2) only if
 // fewer than top_k groups have a larger maximum: no other group can hold one of the
 // top_k, and the smallest maximum of those read again is a bound that few other values
@@ -31,6 +31,7 @@ namespace cg = cooperative_groups;
 typedef unsigned long long u64;
 
 constexpr float NEG_INF = -__builtin_huge_valf();
+constexpr float LOWEST = -3.402823466e38f;
 constexpr float LOG2E = 1.4426950408889634f;
 __device__ __forceinline__ float nan_value() { return __uint_as_float(0x7fc00000u); }
 
@@ -47,8 +48,8 @@ __device__ __forceinline__ float value_of(unsigned o) {
 // Larger value first, then lower index.
 __device__ __forceinline__ u64 key_of(unsigned order, int v) { return ((u64)order << 32) | (unsigned)~v; }
 
-// A row of V elements as vectors of 16 bytes: vector 0 holds the elements before the first
-// 16-byte boundary (0 .. N - 1 of them), vectors 1 .. full are whole, vector full + 1 the rest.
+// A row of V elements as vectors of 16 bytes: 0 .. full - 1 are whole and aligned, full holds
+// the elements before them (0 .. N - 1), full + 1 those after them.
 template <typename T>
 struct RowVecs {
     static constexpr int N = 16 / sizeof(T);
@@ -58,9 +59,8 @@ struct RowVecs {
         full = (V - head) / N;
     }
     __device__ __forceinline__ int count() const { return full + 2; }
-    __device__ __forceinline__ int first(int i) const { return i == 0 ? 0 : head + (i - 1) * N; }
-    __device__ __forceinline__ int last(int i) const { return i == 0 ? head : min(V, head + i * N); }
-    __device__ __forceinline__ bool whole(int i) const { return (unsigned)(i - 1) < (unsigned)full; }
+    __device__ __forceinline__ int first(int i) const { return i == full ? 0 : head + min(i, full) * N; }
+    __device__ __forceinline__ int last(int i) const { return i < full ? head + (i + 1) * N : i == full ? head : V; }
 };
 
 __device__ __forceinline__ void unpack(const uint4& q, float (&f)[8], bf16) {
@@ -123,10 +123,10 @@ __device__ __noinline__ void scatter_vec(T* row, const RowVecs<T> rv, int i, uin
         if (a + j < b) row[a + j] = u.t[j];
 }
 
-// Vector i's bits; what lies outside the row (and a vector past the end) is -inf.
+// Vector i's bits (none at or past `end`).
 template <typename T>
 __device__ __forceinline__ uint4 load_vec(const T* row, const RowVecs<T>& rv, int i, int end) {
-    if (i < end && rv.whole(i)) return __ldg(reinterpret_cast<const uint4*>(row + rv.head) + (i - 1));
+    if (i < min(end, rv.full)) return __ldg(reinterpret_cast<const uint4*>(row + rv.head) + i);
     return gather_vec(row, rv, i, end);
 }
 
@@ -194,7 +194,7 @@ struct Sums {
                 if (MASKED) {
                     float d0, d1;
                     upk2(d2, d0, d1);
-                    d2 = pk2(fmaxf(d0, -3.402823466e38f), fmaxf(d1, -3.402823466e38f));
+                    d2 = pk2(fmaxf(d0, LOWEST), fmaxf(d1, LOWEST));
                 }
                 s2 = add2(s2, e2);
                 w2 = fma2(e2, d2, w2);
@@ -205,10 +205,6 @@ struct Sums {
         upk2(w2, w0, w1);
         s = s0 + s1;
         w = w0 + w1;
-    }
-    __device__ __forceinline__ Sums shuffled(int mask) const {
-        return {__shfl_xor_sync(0xffffffffu, m, mask), __shfl_xor_sync(0xffffffffu, s, mask),
-                __shfl_xor_sync(0xffffffffu, w, mask)};
     }
 };
 
@@ -225,12 +221,16 @@ __device__ __forceinline__ void insert(u64& list, u64 key, bool pass) {
     }
 }
 
+// Neighbouring threads of a group, for 64 groups a block.
+template <int NT>
+constexpr int GROUP_OF = NT / 64;
+
 template <int NT>
 struct ForwardSmem {
-    alignas(16) unsigned group[NT / 4];   // order of each group's largest value
+    alignas(16) unsigned group[64];       // order of each group's largest value
     u64 cand[NT];                         // the warps' lists, packed
     Sums sums[NT / 32];
-    int again[NT / 4];                    // first threads of the groups to read again
+    int again[64];                        // first threads of the groups to read again
     unsigned bound;
     int n_cand, n_again;
     // of the cluster's first block: every block's results
@@ -251,22 +251,24 @@ __device__ __forceinline__ void for_top(const u64* keys, int n, int k, int nt, F
 }
 
 // Leaves in sm.cand (sm.n_cand of them, visible to the block) keys among which are the
-// block's top_k. order: the largest of the thread's group, as in sm.group.
+// block's top_k.
 template <typename T, int NT>
 __device__ __forceinline__ void top_of_block(ForwardSmem<NT>& sm, const T* x, const RowVecs<T>& rv, int begin, int end,
-                                             unsigned order, int top_k) {
-    constexpr int N = RowVecs<T>::N;
+                                             int top_k) {
+    constexpr int N = RowVecs<T>::N, GROUP = GROUP_OF<NT>;
     const int tid = threadIdx.x, lane = tid & 31;
-    int above = 0;
+    if (tid < 64) {
+        const unsigned order = sm.group[tid];
+        int above = 0;
 #pragma unroll
-    for (int j = 0; j < NT / 4; j += 4) {
-        const uint4 g = *reinterpret_cast<const uint4*>(sm.group + j);
-        above += (g.x > order) + (g.y > order) + (g.z > order) + (g.w > order);
-    }
-    const bool again = above < top_k;
-    if (again && (tid & 3) == 0) {
-        atomicMin(&sm.bound, order);
-        sm.again[atomicAdd(&sm.n_again, 1)] = tid;
+        for (int j = 0; j < 64; j += 4) {
+            const uint4 g = *reinterpret_cast<const uint4*>(sm.group + j);
+            above += (g.x > order) + (g.y > order) + (g.z > order) + (g.w > order);
+        }
+        if (above < top_k) {
+            atomicMin(&sm.bound, order);
+            sm.again[atomicAdd(&sm.n_again, 1)] = tid * GROUP;
+        }
     }
     __syncthreads();
     const unsigned bound = sm.bound;
@@ -275,13 +277,13 @@ __device__ __forceinline__ void top_of_block(ForwardSmem<NT>& sm, const T* x, co
     if (n_again <= 2 * top_k) {
         // a thread takes single vectors of all the groups
         constexpr int R = 4;
-        for (int k0 = tid; k0 < n_again * steps * 4; k0 += R * NT) {
+        for (int k0 = tid; k0 < n_again * steps * GROUP; k0 += R * NT) {
             uint4 q[R];
             int at[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int k = k0 + r * NT, g = k / (4 * steps);
-                at[r] = g < n_again ? begin + (k % (4 * steps)) / 4 * NT + sm.again[g] + (k & 3) : end;
+                const int k = k0 + r * NT, step = k / GROUP % steps, g = k / GROUP / steps;
+                at[r] = g < n_again ? begin + step * NT + sm.again[g] + k % GROUP : end;
                 q[r] = load_vec(x, rv, at[r], end);
             }
 #pragma unroll
@@ -311,18 +313,18 @@ __device__ __forceinline__ void top_of_block(ForwardSmem<NT>& sm, const T* x, co
         __syncthreads();
     }
     u64 list = 0;
-    // 32 lanes read a group's four vectors (one step of the pass), or two steps' of them
-    constexpr int STEPS = 32 / (4 * N);
-    for (unsigned todo = __ballot_sync(0xffffffffu, again && (tid & 3) == 0); todo; todo &= todo - 1) {
-        const int g0 = (tid & ~31) + __ffs(todo) - 1;
-        const int mine = g0 + (lane / N) % 4, j = lane % N;
+    // 32 lanes read a group's vectors of STEPS steps
+    constexpr int STEPS = 32 / (GROUP * N);
+    for (int g = tid >> 5; g < 64; g += NT / 32) {
+        if (sm.group[g] < bound) continue;
+        const int mine = g * GROUP + (lane / N) % GROUP, j = lane % N;
         constexpr int R = 8;
         for (int i0 = begin; i0 < end; i0 += R * STEPS * NT) {
             float v[R];
             int at[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int i = i0 + (r * STEPS + lane / (4 * N)) * NT + mine;
+                const int i = i0 + (r * STEPS + lane / (GROUP * N)) * NT + mine;
                 at[r] = -1;
                 v[r] = 0.f;
                 if (i < end) {
@@ -355,7 +357,7 @@ template <typename T, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(NT) token_logprobs_kernel(const T* __restrict__ logits, long long ld, int V,
                                                             float inv_tau, const int* __restrict__ targets,
                                                             LogprobOut out, int parts, unsigned* status) {
-    constexpr int U = 4;
+    constexpr int U = 4, GROUP = GROUP_OF<NT>;
     __shared__ ForwardSmem<NT> sm;
     const int tid = threadIdx.x, lane = tid & 31;
     const int row = CLUSTER ? blockIdx.x / parts : blockIdx.x, part = CLUSTER ? blockIdx.x % parts : 0;
@@ -370,24 +372,47 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const T* __restrict_
         sm.n_cand = sm.n_again = 0;
     }
 
-    Sums a = {-3.402823466e38f, 0.f, 0.f};
+    Sums a = {LOWEST, 0.f, 0.f};
     float largest = NEG_INF;
-    for (int i = begin + tid; i < end; i += U * NT) {
-        uint4 q[U];
-        if (i > 0 && i + (U - 1) * NT < min(end, rv.full + 1)) {
-            const uint4* at = reinterpret_cast<const uint4*>(x + rv.head) + (i - 1);
-#pragma unroll
-            for (int u = 0; u < U; ++u) q[u] = __ldg(at + u * NT);
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u) q[u] = load_vec(x, rv, i + u * NT, end);
-        }
+    auto take = [&](const auto& q) {
         float top, low;
         extremes(q, top, low, T());
         largest = fmaxf(largest, top);
         if (top > a.m) a.raise(top, c);
         if (low > -1e30f) a.add<false, T>(q, c);
         else a.add<true, T>(q, c);
+    };
+    int i = begin + tid;
+    {
+        // batches of U whole vectors, the next one's loads under way
+        const uint4* at = reinterpret_cast<const uint4*>(x + rv.head);
+        const int stop = min(end, rv.full) - (U - 1) * NT;
+        uint4 q[U];
+        if (i < stop) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = __ldg(at + i + u * NT);
+        }
+        for (; i < stop; i += U * NT) {
+            uint4 next[U];
+            if (i + U * NT < stop) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) next[u] = __ldg(at + i + (U + u) * NT);
+            }
+            take(q);
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = next[u];
+        }
+        // what is left: fewer than U vectors, and the row's ends
+        if (i < end) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = load_vec(x, rv, i + u * NT, end);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i + u * NT >= end) break;
+                const uint4 one[1] = {q[u]};
+                take(one);
+            }
+        }
     }
 
     unsigned order = 0;   // of this thread's largest value, then of its group's
@@ -397,18 +422,35 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const T* __restrict_
             for (int i = begin + tid; i < end; i += NT)
                 for (int v = rv.first(i); v < rv.last(i); ++v) order = max(order, order_of(to_f(x[v])));
         }
-        order = max(order, __shfl_xor_sync(0xffffffffu, order, 1));
-        order = max(order, __shfl_xor_sync(0xffffffffu, order, 2));
-        if ((tid & 3) == 0) sm.group[tid >> 2] = order;
+#pragma unroll
+        for (int o = 1; o < GROUP; o *= 2) order = max(order, __shfl_xor_sync(0xffffffffu, order, o));
+        if (tid % GROUP == 0) sm.group[tid / GROUP] = order;
     }
+    // the block's maximum first, so that every thread rescales once
+    {
+        const float wm = warp_max(a.m);
+        if (lane == 0) sm.sums[tid >> 5].m = wm;
+        __syncthreads();
+        float m = sm.sums[0].m;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) a.join(a.shuffled(o), c);
-    if (lane == 0) sm.sums[tid >> 5] = a;
-    __syncthreads();
-    a = sm.sums[0];
+        for (int w = 1; w < NT / 32; ++w) m = fmaxf(m, sm.sums[w].m);
+        a.raise(m, c);
+        a.s = warp_sum(a.s);
+        a.w = warp_sum(a.w);
+        if (lane == 0) {
+            sm.sums[tid >> 5].s = a.s;
+            sm.sums[tid >> 5].w = a.w;
+        }
+        __syncthreads();
+        a.s = sm.sums[0].s;
+        a.w = sm.sums[0].w;
 #pragma unroll
-    for (int w = 1; w < NT / 32; ++w) a.join(sm.sums[w], c);
-    if (out.top_k && (CLUSTER || a.s != 0.f)) top_of_block<T, NT>(sm, x, rv, begin, end, order, out.top_k);
+        for (int w = 1; w < NT / 32; ++w) {
+            a.s += sm.sums[w].s;
+            a.w += sm.sums[w].w;
+        }
+    }
+    if (out.top_k && (CLUSTER || a.s != 0.f)) top_of_block<T, NT>(sm, x, rv, begin, end, out.top_k);
     const u64* keys = sm.cand;
     int n_keys = sm.n_cand;
     if (CLUSTER) {
@@ -482,29 +524,38 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, lo
     const float gt = g * inv_tau, A = -(g + h * H) * inv_tau, B = -h * inv_tau;
     const RowVecs<T> rv(dx, V);   // the vectors of what is written
     const int per = ceil_div(rv.count(), parts), end = min(rv.count(), (part + 1) * per);
+    // whole vectors where x has the boundaries of dx, else element by element
+    const int whole = (((uintptr_t)x ^ (uintptr_t)dx) & 15) == 0 ? min(end, rv.full) : 0;
+    const uint4* from = reinterpret_cast<const uint4*>(x + rv.head);
+    uint4* to = reinterpret_cast<uint4*>(dx + rv.head);
     const int i0 = part * per + threadIdx.x;
-    const bool same = (((uintptr_t)x ^ (uintptr_t)dx) & 15) == 0;
-    // a thread's vectors i0, i0 + 256, ..: at most U of them (`parts`)
-    uint4 q[U];
-    if (!none) {
+    if (none) {
+        for (int i = i0; i < end; i += 256) {
+            if (i < rv.full) to[i] = make_uint4(0, 0, 0, 0);
+            else scatter_vec(dx, rv, i, make_uint4(0, 0, 0, 0));
+        }
+        return;
+    }
+    auto load = [&](uint4 (&q)[U], int i) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = i0 + u * 256;
-            if (k < end && rv.whole(k) && same) q[u] = *(reinterpret_cast<const uint4*>(x + rv.head) + (k - 1));
-            else q[u] = gather_vec(x, rv, k, end);
+            const int k = i + u * 256;
+            if (k < whole) q[u] = from[k];
+            else if (k < end) q[u] = gather_vec(x, rv, k, end);
         }
-    }
+    };
+    const f32x2 it2 = pk2(inv_tau, inv_tau), l2 = pk2(-L, -L), e2 = pk2(LOG2E, LOG2E), A2 = pk2(A, A), B2 = pk2(B, B);
+    uint4 q[U];
+    load(q, i0);
+    for (int i = i0; i < end; i += U * 256) {
+        uint4 next[U];
+        load(next, i + U * 256);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int k = i0 + u * 256;
-        if (k >= end) break;
-        const int first = rv.first(k);
-        if (none) {
-            q[u] = make_uint4(0, 0, 0, 0);
-        } else {
+        for (int u = 0; u < U; ++u) {
+            const int k = i + u * 256;
+            if (k >= end) break;
             float r[N];
             unpack(q[u], r, T());
-            const f32x2 it2 = pk2(inv_tau, inv_tau), l2 = pk2(-L, -L), e2 = pk2(LOG2E, LOG2E), A2 = pk2(A, A), B2 = pk2(B, B);
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
                 const f32x2 d2 = fma2(pk2(r[j], r[j + 1]), it2, l2);
@@ -515,18 +566,17 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, lo
                 const f32x2 f2 = fma2(B2, pk2(fmaxf(d0, -1e30f), fmaxf(d1, -1e30f)), A2);
                 upk2(mul2(pk2(ex2_approx(y0), ex2_approx(y1)), f2), r[j], r[j + 1]);
             }
-            if ((unsigned)(t - first) < (unsigned)N) {
+            const int at = t - rv.first(k);
+            if ((unsigned)at < (unsigned)N && t < rv.last(k)) {
 #pragma unroll
                 for (int j = 0; j < N; ++j)
-                    if (first + j == t) r[j] += gt;
+                    if (j == at) r[j] += gt;
             }
-            q[u] = pack(r, T());
+            if (k < rv.full) to[k] = pack(r, T());
+            else scatter_vec(dx, rv, k, pack(r, T()));
         }
-        if (rv.whole(k)) {
-            *(reinterpret_cast<uint4*>(dx + rv.head) + (k - 1)) = q[u];
-        } else {
-            scatter_vec(dx, rv, k, q[u]);
-        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[u] = next[u];
     }
 }
 
@@ -559,10 +609,7 @@ void launch_forward(const Ctx& ctx, const T* logits, long long ld, int rows, int
 template <typename T>
 void launch_token_logprobs(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float temperature,
                            const int* targets, const LogprobOut& out) {
-    if (V >= 4096)
-        launch_forward<T, 256>(ctx, logits, ld, rows, V, 1.f / temperature, targets, out);
-    else
-        launch_forward<T, 128>(ctx, logits, ld, rows, V, 1.f / temperature, targets, out);
+    launch_forward<T, 128>(ctx, logits, ld, rows, V, 1.f / temperature, targets, out);
     ++*ctx.launches;
 }
 
@@ -570,7 +617,11 @@ template <typename T>
 void launch_token_logprobs_bwd(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float temperature,
                                const int* targets, const float* lse, const float* dlogp, const float* entropy,
                                const float* dentropy, T* dlogits, long long ldd) {
-    const int parts = ceil_div(V / RowVecs<T>::N + 2, 1024);   // four vectors a thread
+    // sixteen vectors a thread; fewer, down to two, where that leaves an SM less than eight blocks
+    const int vecs = V / RowVecs<T>::N + 2;
+    int per = 16;
+    while (per > 2 && (long long)rows * ceil_div(vecs, 256 * per) < 8 * ctx.num_sms) per /= 2;
+    const int parts = ceil_div(vecs, 256 * per);
     token_logprobs_bwd_kernel<T><<<rows * parts, 256, 0, ctx.stream>>>(logits, ld, V, 1.f / temperature, targets, lse,
                                                                        dlogp, entropy, dentropy, dlogits, ldd, parts,
                                                                        ctx.status);
