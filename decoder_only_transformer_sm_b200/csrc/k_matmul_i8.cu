@@ -31,6 +31,28 @@ __device__ __forceinline__ O finish(int acc, float sa, float sb, float bias, flo
     return from_f<O>(u);
 }
 
+// Two at a time, in packed arithmetic (the same operations and roundings).
+template <int KIND, typename O>
+__device__ __forceinline__ f32x2 finish2(int a0, int a1, f32x2 sa, f32x2 sb, f32x2 bias, f32x2 resid) {
+    f32x2 u = mul2(pk2((float)a0, (float)a1), sa);
+    u = KIND == EPI_STORE ? mul2(u, sb) : fma2(u, sb, bias);
+    if (KIND == EPI_BIAS_RESID) u = add2(u, resid);
+    if (KIND == EPI_BIAS_GELU) {
+        float x, y;
+        upk2(u, x, y);
+        if (sizeof(O) == 4) {
+            u = pk2(gelu_tanh(x), gelu_tanh(y));
+        } else {   // u / (1 + 2^(u (K1 + K2 u^2))), the logistic form of the tanh one
+            constexpr float K1 = -2.0f * 0.7978845608028654f * 1.4426950408889634f, K2 = K1 * 0.044715f;
+            float e0, e1;
+            upk2(mul2(u, fma2(mul2(u, u), pk2(K2, K2), pk2(K1, K1))), e0, e1);
+            upk2(add2(pk2(ex2_approx(e0), ex2_approx(e1)), pk2(1.f, 1.f)), e0, e1);
+            u = mul2(u, pk2(rcp_approx(e0), rcp_approx(e1)));
+        }
+    }
+    return u;
+}
+
 // ---------------------------------------------------------------- any strides
 // 64 x 64 outputs per block of 256 threads (4 x 4 each), 64 bytes of K staged at a
 // time as 32-bit words for dp4a. Rows may start at any byte: words are put together
@@ -167,21 +189,26 @@ void launch_rows(const Ctx& ctx, const I8Product& p) {
 }
 
 // ---------------------------------------------------------------- tensor cores
-// Persistent kernel, a CTA walks output tiles of 128 x BN. Warp 0 streams 128-byte-wide
-// K blocks of both operands with TMA into a ring of STAGES; warp 1 issues tcgen05.mma
-// (kind::i8, 128 x BN x 32) into one of two int32 accumulators in tensor memory; the epilogue
-// warps read the other one (a lane is a row), scale it and turn it around in a swizzled
-// shared-memory buffer of their own, so that memory sees whole 128-byte row segments. Rows and
-// columns past the operands come as zeros from TMA and are not stored.
-template <int BN>
+// Persistent kernel: a CTA, or a pair of CTAs (a cluster of two, cta_group::2), walks output
+// tiles of 128 CTAS x BN. Warp 0 streams 128-byte-wide K blocks of both operands with TMA into a
+// ring of STAGES; warp 1 (of the pair's first CTA) issues tcgen05.mma (kind::i8, 128 CTAS x BN x 32)
+// into one of two int32 accumulators in tensor memory; the epilogue warps read the other one (a lane
+// is a row), scale it and hand it, 32 rows of 128 bytes at a time, to TMA stores from two buffers
+// each (or, where rows of the result are not whole 16-byte segments, store it themselves). Rows and columns past the operands come as zeros from TMA and are not stored.
+// A pair shares its B rows, so a K block costs each CTA 32 KB of shared memory and of L2
+// traffic for 256 x 256 outputs a pair, where one CTA alone needs 48 KB for 128 x 256.
+template <int BN, int CTAS>
 struct Tile {
-    static constexpr int BM = 128, BK = 128;
-    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-    static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
+    static constexpr int BM = 128, BK = 128;   // rows of a CTA
+    static constexpr int B_ROWS = BN / CTAS;   // B rows in a CTA's shared memory
+    static constexpr int A_BYTES = BM * BK, B_BYTES = B_ROWS * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES = BN >= 128 ? 4 : 8;
+    static constexpr int EPI_WARPS = BN >= 256 ? 16 : BN >= 128 ? 8 : 4;
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int WCOLS = BN / (EPI_WARPS / 4);   // columns of a warp
     static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int EPI_BUFS = BN >= 256 ? 1 : 2;   // a warp's staging buffers
+    static constexpr int EPI_COLS = 8 * WCOLS;           // bytes of a warp's column scales and biases
 };
 
 struct TileCtl {
@@ -189,13 +216,11 @@ struct TileCtl {
     uint32_t tmem_base, abort;
 };
 
-constexpr int EPI_ROWS = 32 * 128;   // a warp's staging: 32 rows of 128 bytes
-constexpr int EPI_COLS = 256;        // and 32 columns' scales and biases
+constexpr int EPI_ROWS = 32 * 128;   // a staging buffer: 32 rows of 128 bytes
 
-template <int BN>
+template <typename L>
 constexpr size_t tile_smem() {
-    return (size_t)Tile<BN>::STAGES * Tile<BN>::STAGE_BYTES + Tile<BN>::EPI_WARPS * (EPI_ROWS + EPI_COLS) +
-           sizeof(TileCtl) + 16;
+    return (size_t)L::STAGES * L::STAGE_BYTES + L::EPI_WARPS * (L::EPI_BUFS * EPI_ROWS + L::EPI_COLS) + sizeof(TileCtl) + 16;
 }
 
 struct TileGrid {
@@ -248,17 +273,36 @@ __device__ __forceinline__ void move_rows(uint8_t* buf, E* mem, long long ld, in
     }
 }
 
-template <int KIND, typename O, int BN>
-__global__ void __launch_bounds__(Tile<BN>::THREADS, 1)
-    matmul_i8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, I8Product p,
-                        TileGrid grid, unsigned* status) {
-    using L = Tile<BN>;
+// 16 bytes of results.
+__device__ __forceinline__ void put(uint8_t* at, const f32x2 (&v)[2], float) {
+    *reinterpret_cast<ulonglong2*>(at) = ulonglong2{v[0], v[1]};
+}
+__device__ __forceinline__ void put(uint8_t* at, const f32x2 (&v)[4], bf16) {
+    unsigned u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float x, y;
+        upk2(v[i], x, y);
+        const __nv_bfloat162 t = __floats2bfloat162_rn(x, y);
+        u[i] = *reinterpret_cast<const unsigned*>(&t);
+    }
+    *reinterpret_cast<uint4*>(at) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+template <int KIND, typename O, int BN, int CTAS>
+__global__ void __launch_bounds__(Tile<BN, CTAS>::THREADS, 1)
+    matmul_i8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmO, I8Product p, TileGrid grid, unsigned* status) {
+    using L = Tile<BN, CTAS>;
+    constexpr bool PAIR = CTAS == 2;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* epi = smem + L::STAGES * L::STAGE_BYTES;
-    TileCtl* ctl = reinterpret_cast<TileCtl*>(epi + L::EPI_WARPS * (EPI_ROWS + EPI_COLS));
+    TileCtl* ctl = reinterpret_cast<TileCtl*>(epi + L::EPI_WARPS * (L::EPI_BUFS * EPI_ROWS + L::EPI_COLS));
     volatile uint32_t* abort = &ctl->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = grid.tiles_m * grid.tiles_n;
+    const int rank = PAIR ? (int)tc::cluster_rank() : 0;
+    const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::STAGES; ++s) {
@@ -267,18 +311,25 @@ __global__ void __launch_bounds__(Tile<BN>::THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&ctl->acc_full[b], 1);
-            tc::mbar_init(&ctl->acc_empty[b], L::EPI_WARPS);
+            tc::mbar_init(&ctl->acc_empty[b], CTAS * L::EPI_WARPS);
         }
         tc::mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
         tc::fence_barrier_init();
     }
     if (warp == 1) {
-        tc::tmem_alloc(&ctl->tmem_base, L::TMEM_COLS);
-        tc::tmem_relinquish();
+        if (PAIR) {
+            tc::tmem_alloc_pair(&ctl->tmem_base, L::TMEM_COLS);
+            tc::tmem_relinquish_pair();
+        } else {
+            tc::tmem_alloc(&ctl->tmem_base, L::TMEM_COLS);
+            tc::tmem_relinquish();
+        }
     }
     tc::fence_before_sync();
-    __syncthreads();
+    __syncwarp();
+    if (PAIR) tc::cluster_sync();
+    else __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = ctl->tmem_base;
 
@@ -288,40 +339,55 @@ __global__ void __launch_bounds__(Tile<BN>::THREADS, 1)
             tc::tma_prefetch_desc(&tmB);
             uint32_t it = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < tiles && ok; u += gridDim.x) {
+            for (int u = first; u < tiles && ok; u += step) {
                 int mb, nb;
                 grid.at(u, mb, nb);
+                const int m0 = (mb * CTAS + rank) * L::BM, n0 = nb * BN + rank * L::B_ROWS;
                 for (int kb = 0; kb < grid.k_blocks; ++kb, ++it) {
                     const int s = it % L::STAGES;
                     if (!tc::mbar_wait(&ctl->empty[s], ((it / L::STAGES) & 1) ^ 1, abort, status)) {
                         ok = false;
                         break;
                     }
-                    tc::mbar_expect_tx(&ctl->full[s], L::STAGE_BYTES);
                     uint8_t* sa = smem + s * L::STAGE_BYTES;
-                    tc::tma_load_2d(sa, &tmA, kb * L::BK, mb * L::BM, &ctl->full[s]);
-                    tc::tma_load_2d(sa + L::A_BYTES, &tmB, kb * L::BK, nb * BN, &ctl->full[s]);
+                    if (PAIR) {
+                        // both CTAs' bytes are counted on the first one's barrier
+                        const uint32_t bar = tc::map_rank(&ctl->full[s], 0);
+                        if (rank == 0) tc::mbar_expect_tx(&ctl->full[s], 2 * L::STAGE_BYTES);
+                        tc::tma_load_2d_pair(sa, &tmA, kb * L::BK, m0, bar);
+                        tc::tma_load_2d_pair(sa + L::A_BYTES, &tmB, kb * L::BK, n0, bar);
+                    } else {
+                        tc::mbar_expect_tx(&ctl->full[s], L::STAGE_BYTES);
+                        tc::tma_load_2d(sa, &tmA, kb * L::BK, m0, &ctl->full[s]);
+                        tc::tma_load_2d(sa + L::A_BYTES, &tmB, kb * L::BK, n0, &ctl->full[s]);
+                    }
                 }
             }
             if (!ok) {   // given up: nobody may wait for the loads in flight, and they must land before the CTA ends
                 volatile uint32_t no_abort = 0;
-                for (uint32_t j = it > L::STAGES ? it - L::STAGES : 0; j < it; ++j)
-                    tc::mbar_wait(&ctl->full[j % L::STAGES], (j / L::STAGES) & 1, &no_abort, status);
+                if (rank == 0) {
+                    for (uint32_t j = it > L::STAGES ? it - L::STAGES : 0; j < it; ++j)
+                        tc::mbar_wait(&ctl->full[j % L::STAGES], (j / L::STAGES) & 1, &no_abort, status);
+                } else {   // their barrier is the other CTA's: 1 ms
+                    const unsigned long long t0 = tc::globaltimer();
+                    while (tc::globaltimer() - t0 < 1000000ull) {
+                    }
+                }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = tc::idesc_i8_s32(L::BM, BN);
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = tc::idesc_i8_s32(L::BM * CTAS, BN);
             uint32_t it = 0, acc_it = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < tiles && ok; u += gridDim.x, ++acc_it) {
+            for (int u = first; u < tiles && ok; u += step, ++acc_it) {
                 const uint32_t ab = acc_it & 1;
-                if (!tc::mbar_wait(&ctl->acc_empty[ab], ((acc_it >> 1) & 1) ^ 1, abort, status)) break;
+                if (!tc::mbar_wait_cluster(&ctl->acc_empty[ab], ((acc_it >> 1) & 1) ^ 1, abort, status)) break;
                 tc::fence_after_sync();
                 const uint32_t d_tmem = tmem + ab * BN;
                 for (int kb = 0; kb < grid.k_blocks; ++kb, ++it) {
                     const int s = it % L::STAGES;
-                    if (!tc::mbar_wait(&ctl->full[s], (it / L::STAGES) & 1, abort, status)) {
+                    if (!tc::mbar_wait_cluster(&ctl->full[s], (it / L::STAGES) & 1, abort, status)) {
                         ok = false;
                         break;
                     }
@@ -331,42 +397,74 @@ __global__ void __launch_bounds__(Tile<BN>::THREADS, 1)
                     for (int kk = 0; kk < L::BK / 32; ++kk) {
                         const uint64_t da = tc::smem_desc_sw128(a_base + kk * 32, 16, 1024);
                         const uint64_t db = tc::smem_desc_sw128(a_base + L::A_BYTES + kk * 32, 16, 1024);
-                        tc::mma_i8(d_tmem, da, db, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                        if (PAIR) tc::mma_i8_pair(d_tmem, da, db, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                        else tc::mma_i8(d_tmem, da, db, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
                     }
-                    tc::mma_commit(&ctl->empty[s]);
+                    if (PAIR) tc::mma_commit_pair(&ctl->empty[s]);
+                    else tc::mma_commit(&ctl->empty[s]);
                 }
-                tc::mma_commit(&ctl->acc_full[ab]);
+                if (PAIR) tc::mma_commit_pair(&ctl->acc_full[ab]);
+                else tc::mma_commit(&ctl->acc_full[ab]);
             }
             // every MMA issued has completed once `drain` fires; this wait ignores an abort (TMEM must not
             // be freed under running MMAs) but is bounded in time
             volatile uint32_t no_abort = 0;
-            tc::mma_commit(&ctl->drain);
-            tc::mbar_wait(&ctl->drain, 0, &no_abort, status);
+            if (PAIR) tc::mma_commit_pair(&ctl->drain);
+            else tc::mma_commit(&ctl->drain);
+            tc::mbar_wait_cluster(&ctl->drain, 0, &no_abort, status);
         }
     } else {
-        constexpr int FULL = 128 / (int)sizeof(O), CW = L::WCOLS < FULL ? L::WCOLS : FULL;   // columns of a staged chunk
+        constexpr int FULL = 128 / (int)sizeof(O), CW = L::WCOLS < FULL ? L::WCOLS : FULL;   // columns of a chunk
         constexpr int PER = 16 / sizeof(O);
+        constexpr bool TMA_OUT = CW * sizeof(O) == 128;
+        const bool tma_out = TMA_OUT && grid.vec_out;
         const int ew = warp - 2, quarter = warp & 3, cbase = (ew >> 2) * L::WCOLS;
-        uint8_t* buf = epi + ew * EPI_ROWS;
-        float* cols = reinterpret_cast<float*>(epi + L::EPI_WARPS * EPI_ROWS + ew * EPI_COLS);
-        uint32_t acc_it = 0;
-        for (int u = blockIdx.x; u < tiles; u += gridDim.x, ++acc_it) {
+        uint8_t* bufs = epi + ew * L::EPI_BUFS * EPI_ROWS;
+        float* cols = reinterpret_cast<float*>(epi + L::EPI_WARPS * L::EPI_BUFS * EPI_ROWS + ew * L::EPI_COLS);
+        constexpr int NC = L::WCOLS / 32;
+        // of the next tile: its row's scale, and the scales and biases of columns lane, lane + 32, ..
+        float sa = 0.f, sb[NC], bias[NC];
+        auto fetch = [&](int u) {
+            if (u >= tiles) return;
+            int mb, nb;
+            grid.at(u, mb, nb);
+            const int row = (mb * CTAS + rank) * L::BM + quarter * 32 + lane;
+            sa = row < p.M ? __ldg(p.sa + row) : 0.f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int col = nb * BN + cbase + 32 * i + lane;
+                sb[i] = col < p.N ? __ldg(p.sb + col) : 0.f;
+                if (KIND != EPI_STORE) bias[i] = col < p.N ? __ldg(p.bias + col) : 0.f;
+            }
+        };
+        fetch(first);
+        uint32_t acc_it = 0, chunk = 0;
+        for (int u = first; u < tiles; u += step, ++acc_it) {
             int mb, nb;
             grid.at(u, mb, nb);
             const uint32_t ab = acc_it & 1;
-            const int row0 = mb * L::BM + quarter * 32, n0 = nb * BN + cbase;
-            const float sa = row0 + lane < p.M ? p.sa[row0 + lane] : 0.f;
-            // lane l holds the scale and the bias of column l of the next 32
-            auto column = [&](const float* v, int c) { return c + lane < p.N ? __ldg(v + c + lane) : 0.f; };
-            float sb = column(p.sb, n0), bias = KIND != EPI_STORE ? column(p.bias, n0) : 0.f;
+            const int row0 = (mb * CTAS + rank) * L::BM + quarter * 32, n0 = nb * BN + cbase;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                cols[32 * i + lane] = sb[i];
+                if (KIND != EPI_STORE) cols[L::WCOLS + 32 * i + lane] = bias[i];
+            }
+            const f32x2 row_scale = pk2(sa, sa);
+            __syncwarp();
+            fetch(u + step);
             uint32_t ok = 0;
-            if (lane == 0) ok = tc::mbar_wait(&ctl->acc_full[ab], (acc_it >> 1) & 1, abort, status) ? 1u : 0u;
+            if (lane == 0) ok = tc::mbar_wait_cluster(&ctl->acc_full[ab], (acc_it >> 1) & 1, abort, status) ? 1u : 0u;
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             tc::fence_after_sync();
             const uint32_t taddr = tmem + ab * BN + cbase + ((uint32_t)(quarter * 32) << 16);
-#pragma unroll 1
-            for (int c0 = 0; c0 < L::WCOLS; c0 += CW) {
+#pragma unroll
+            for (int c0 = 0; c0 < L::WCOLS; c0 += CW, ++chunk) {
                 if (n0 + c0 >= p.N || row0 >= p.M) break;
+                uint8_t* buf = bufs + (chunk % L::EPI_BUFS) * EPI_ROWS;
+                if (tma_out) {   // the buffer's last store has read it
+                    if (lane == 0) tc::bulk_wait_read<L::EPI_BUFS - 1>();
+                    __syncwarp();
+                }
                 if (KIND == EPI_BIAS_RESID) {
                     move_rows<float, CW, false>(buf, const_cast<float*>(p.resid), p.ldr, row0, n0 + c0, p.M, p.N,
                                                 grid.vec_resid);
@@ -374,46 +472,60 @@ __global__ void __launch_bounds__(Tile<BN>::THREADS, 1)
                 }
 #pragma unroll
                 for (int h = 0; h < CW; h += 32) {
-                    cols[lane] = sb;
-                    if (KIND != EPI_STORE) cols[32 + lane] = bias;
-                    __syncwarp();
-                    const int next = n0 + c0 + h + 32;
-                    sb = column(p.sb, next);
-                    if (KIND != EPI_STORE) bias = column(p.bias, next);
                     float acc[32];
                     tc::tmem_ld_32x32b_x32(taddr + c0 + h, acc);
 #pragma unroll
                     for (int c = 0; c < 32; c += PER) {
-                        alignas(16) O v[PER];
                         uint8_t* at = buf + seg(lane, (h + c) / PER);
-                        const float4 in = KIND == EPI_BIAS_RESID ? *reinterpret_cast<const float4*>(at)
-                                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
-                        const float r[4] = {in.x, in.y, in.z, in.w};
+                        f32x2 v[PER / 2], in[2] = {};
+                        if (KIND == EPI_BIAS_RESID) {
+                            const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(at);
+                            in[0] = q.x;
+                            in[1] = q.y;
+                        }
 #pragma unroll
                         for (int i = 0; i < PER; i += 4) {
-                            const float4 s4 = *reinterpret_cast<const float4*>(cols + c + i);
-                            const float4 b4 = KIND != EPI_STORE ? *reinterpret_cast<const float4*>(cols + 32 + c + i)
-                                                                : make_float4(0.f, 0.f, 0.f, 0.f);
-                            v[i] = finish<KIND, O>(__float_as_int(acc[c + i]), sa, s4.x, b4.x, r[0]);
-                            v[i + 1] = finish<KIND, O>(__float_as_int(acc[c + i + 1]), sa, s4.y, b4.y, r[1]);
-                            v[i + 2] = finish<KIND, O>(__float_as_int(acc[c + i + 2]), sa, s4.z, b4.z, r[2]);
-                            v[i + 3] = finish<KIND, O>(__float_as_int(acc[c + i + 3]), sa, s4.w, b4.w, r[3]);
+                            const float* col = cols + c0 + h + c + i;
+                            const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(col);
+                            const ulonglong2 b4 = KIND != EPI_STORE ? *reinterpret_cast<const ulonglong2*>(col + L::WCOLS)
+                                                                    : ulonglong2{0, 0};
+                            const int* a4 = reinterpret_cast<const int*>(acc) + c + i;
+                            v[i / 2] = finish2<KIND, O>(a4[0], a4[1], row_scale, s4.x, b4.x, in[0]);
+                            v[i / 2 + 1] = finish2<KIND, O>(a4[2], a4[3], row_scale, s4.y, b4.y, in[1]);
                         }
-                        *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(v);
+                        put(at, v, O());
                     }
+                }
+                __syncwarp();
+                if (tma_out) {
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::tma_store_2d(&tmO, buf, n0 + c0, row0);
+                        tc::bulk_commit();
+                    }
+                } else {
+                    move_rows<O, CW, true>(buf, reinterpret_cast<O*>(p.out), p.ldo, row0, n0 + c0, p.M, p.N, grid.vec_out);
                     __syncwarp();
                 }
-                move_rows<O, CW, true>(buf, reinterpret_cast<O*>(p.out), p.ldo, row0, n0 + c0, p.M, p.N, grid.vec_out);
-                __syncwarp();
             }
             tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&ctl->acc_empty[ab]);
+            __syncwarp();   // also: the columns' values have been read
+            if (lane == 0) {
+                if (PAIR) tc::mbar_arrive_cluster(tc::map_rank(&ctl->acc_empty[ab], 0));
+                else tc::mbar_arrive(&ctl->acc_empty[ab]);
+            }
         }
+        if (lane == 0) tc::bulk_wait<0>();
     }
     tc::fence_before_sync();
-    __syncthreads();
-    if (warp == 1) tc::tmem_dealloc(tmem, L::TMEM_COLS);
+    __syncwarp();
+    if (PAIR) tc::cluster_sync();   // nobody's shared or tensor memory is used any more
+    else __syncthreads();
+    if (warp == 1) {
+        if (PAIR) tc::tmem_dealloc_pair(tmem, L::TMEM_COLS);
+        else tc::tmem_dealloc(tmem, L::TMEM_COLS);
+    }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -431,16 +543,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return f;
 }
 
-// int8 [rows][K], row stride ld; boxes of 128 bytes x box_rows, 128-byte swizzle.
-bool make_map(CUtensorMap* m, const int8_t* ptr, long long rows, int K, long long ld, int box_rows) {
+// [rows][cols] with row stride ld (elements); boxes of box_cols (128 bytes) x box_rows, 128-byte swizzle.
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, int es, const void* ptr, long long rows, int cols, long long ld,
+              int box_cols, int box_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)ld};
-    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * es};
+    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(ptr), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return fn(m, type, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -457,24 +570,45 @@ void allow_smem(F* kernel, size_t bytes, std::atomic<unsigned long long>& done) 
 
 bool whole_segments(const void* p, long long ld, int es) { return ((uintptr_t)p & 15) == 0 && (ld * es) % 16 == 0; }
 
-template <int KIND, typename O, int BN>
+template <int KIND, typename O, int BN, int CTAS>
 bool launch_tc(const Ctx& ctx, const I8Product& p) {
-    using L = Tile<BN>;
-    CUtensorMap ta, tb;
-    if (!make_map(&ta, p.A, p.M, p.K, p.lda, L::BM) || !make_map(&tb, p.B, p.N, p.K, p.ldb, BN)) return false;
+    using L = Tile<BN, CTAS>;
+    constexpr int FULL = 128 / (int)sizeof(O), CW = L::WCOLS < FULL ? L::WCOLS : FULL;
+    CUtensorMap ta, tb, to;
+    const CUtensorMapDataType I8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     TileGrid g;
-    g.tiles_m = ceil_div(p.M, L::BM);
+    g.tiles_m = ceil_div(p.M, L::BM * CTAS);
     g.tiles_n = ceil_div(p.N, BN);
     g.k_blocks = ceil_div(p.K, L::BK);
     // the operand of the fast index is read again for every slow block: the smaller one, which stays in L2
     g.m_fastest = p.M < p.N;
     g.vec_out = whole_segments(p.out, p.ldo, sizeof(O));
     g.vec_resid = KIND == EPI_BIAS_RESID && whole_segments(p.resid, p.ldr, 4);
+    if (!make_map(&ta, I8, 1, p.A, p.M, p.K, p.lda, L::BK, L::BM) ||
+        !make_map(&tb, I8, 1, p.B, p.N, p.K, p.ldb, L::BK, L::B_ROWS))
+        return false;
+    if (g.vec_out && CW * sizeof(O) == 128) {
+        if (!make_map(&to, sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                      sizeof(O), p.out, p.M, p.N, p.ldo, CW, 32))
+            return false;
+    } else {
+        to = ta;   // not used
+    }
+    auto kernel = matmul_i8_tc_kernel<KIND, O, BN, CTAS>;
     static std::atomic<unsigned long long> done{0};
-    allow_smem(matmul_i8_tc_kernel<KIND, O, BN>, tile_smem<BN>(), done);
-    matmul_i8_tc_kernel<KIND, O, BN><<<min(g.tiles_m * g.tiles_n, ctx.num_sms), L::THREADS, tile_smem<BN>(), ctx.stream>>>(
-        ta, tb, p, g, ctx.status);
-    return true;
+    allow_smem(kernel, tile_smem<L>(), done);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CTAS * min(g.tiles_m * g.tiles_n, ctx.num_sms / CTAS));
+    cfg.blockDim = dim3(L::THREADS);
+    cfg.dynamicSmemBytes = tile_smem<L>();
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CTAS;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = CTAS > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, ta, tb, to, p, g, ctx.status) == cudaSuccess;
 }
 
 template <int KIND, typename O>
@@ -488,13 +622,14 @@ bool launch_kind(const Ctx& ctx, const I8Product& p) {
             else launch_rows<KIND, O, 8>(ctx, p);
             return true;
         }
-        // the widest tile that still gives every SM one
-        const int tiles_m = ceil_div(p.M, 128);
-        auto fills = [&](int bn) { return (long long)tiles_m * ceil_div(p.N, bn) >= ctx.num_sms; };
-        if (fills(256)) return launch_tc<KIND, O, 256>(ctx, p);
-        if (fills(128)) return launch_tc<KIND, O, 128>(ctx, p);
-        if (fills(64)) return launch_tc<KIND, O, 64>(ctx, p);
-        return launch_tc<KIND, O, 32>(ctx, p);
+        // the widest tile that still gives (nearly) every SM one
+        auto fills = [&](int bm, int bn, int units) {
+            return 8ll * ceil_div(p.M, bm) * ceil_div(p.N, bn) >= 7ll * units;
+        };
+        if (fills(256, 256, ctx.num_sms / 2)) return launch_tc<KIND, O, 256, 2>(ctx, p);
+        if (fills(128, 128, ctx.num_sms)) return launch_tc<KIND, O, 128, 1>(ctx, p);
+        if (fills(128, 64, ctx.num_sms)) return launch_tc<KIND, O, 64, 1>(ctx, p);
+        return launch_tc<KIND, O, 32, 1>(ctx, p);
     }
     const long long tiles = (long long)ceil_div(p.N, ST) * ceil_div(p.M, ST);
     matmul_i8_simt_kernel<KIND, O><<<(unsigned)tiles, 256, 0, ctx.stream>>>(p);

@@ -271,7 +271,10 @@ extern "C" int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scal
     p.bias = bias;
     p.resid = resid;
     p.ldr = ldr;
-    if (!launch_matmul_i8(c, p)) return set_error(GPT2_ERR_CUDA, "tensor-map encoding failed");
+    if (!launch_matmul_i8(c, p)) {
+        cudaError_t err = cudaGetLastError();   // read, so that no later call reports it
+        return set_error(GPT2_ERR_CUDA, err != cudaSuccess ? cudaGetErrorString(err) : "tensor-map encoding failed");
+    }
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return set_error(GPT2_ERR_CUDA, cudaGetErrorString(err));
     return GPT2_OK;

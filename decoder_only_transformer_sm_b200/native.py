@@ -459,15 +459,21 @@ def sample(logits, V: int, temperature: float, top_k: int, u, next_tokens, ld: i
 # rows lie further apart than they are long (unit stride inside a row).
 # ---------------------------------------------------------------------------
 # Small calls are bound by the host, so the checks below read each tensor property once.
-_torch = None       # the module and its type codes, set by the first call
-_FLOATS = _INT8 = None
+_torch = None       # the module, its type codes and its raw stream and device getters, set by the first call
+_FLOATS = _INT8 = _raw_stream = _current_device = None
 
 
 def _import_torch():
-    global _torch, _FLOATS, _INT8
+    global _torch, _FLOATS, _INT8, _raw_stream, _current_device
     import torch
     _FLOATS = {torch.float32: 0, torch.bfloat16: 1}
     _INT8 = {torch.int8: 0}
+    # the handle of torch.cuda.current_stream(dev) and torch.cuda.current_device() without a Stream
+    # object and the check for a first use, which the tensors' existence answers
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    load_library()
     _torch = torch
     return torch
 
@@ -516,7 +522,7 @@ def _status_on(dev, stream):
 
 def _call(dev, fn, *args):
     """fn(*args) with device dev current; raises on an error code."""
-    if _torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         rc = fn(*args)
     else:
         with _torch.cuda.device(dev):
@@ -533,8 +539,8 @@ def quantize_rows(x, q, scale, stream=None):
     ps = _vector_of(scale, "scale", torch.float32, rows)
     dev = _device_of(x, q, scale)
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
-    _call(dev, (_lib or load_library()).gpt2k_quantize_rows, code, px, rows, K, ldx, pq, ldq, ps, stream)
+        stream = _raw_stream(dev)
+    _call(dev, _lib.gpt2k_quantize_rows, code, px, rows, K, ldx, pq, ldq, ps, stream)
 
 
 def matmul_i8(A, a_scale, B, b_scale, out, epilogue: str = "store", bias=None, resid=None, status=None, stream=None):
@@ -554,10 +560,10 @@ def matmul_i8(A, a_scale, B, b_scale, out, epilogue: str = "store", bias=None, r
     pbias = _vector_of(bias, "bias", f32, N)
     dev = _device_of(A, a_scale, B, b_scale, out, bias, resid, status)
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = _raw_stream(dev)
     if status is None:
         status = _status_on(dev, stream)
-    _call(dev, (_lib or load_library()).gpt2k_matmul_i8, pa, lda, psa, pb, ldb, psb, M, N, K, EPILOGUE[epilogue],
+    _call(dev, _lib.gpt2k_matmul_i8, pa, lda, psa, pb, ldb, psb, M, N, K, EPILOGUE[epilogue],
           code, po, ldo, pbias, pr, ldr, status.data_ptr(), stream)
     return status
 
@@ -578,10 +584,10 @@ def token_logprobs(logits, V: int, temperature: float, targets=None, logp=None, 
     pi, pp = _vector_of(top_ids, "top_ids", i32, rows * k), _vector_of(top_logp, "top_logp", f32, rows * k)
     dev = _device_of(logits, targets, logp, entropy, lse, top_ids, top_logp, status)
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = _raw_stream(dev)
     if status is None:
         status = _status_on(dev, stream)
-    _call(dev, (_lib or load_library()).gpt2k_token_logprobs, code, px, rows, V, ld, temperature, pt, k, pl, pe, ps,
+    _call(dev, _lib.gpt2k_token_logprobs, code, px, rows, V, ld, temperature, pt, k, pl, pe, ps,
           pi, pp, status.data_ptr(), stream)
     return status
 
@@ -603,9 +609,9 @@ def token_logprobs_bwd(logits, V: int, temperature: float, lse, dlogits, targets
     ph = _vector_of(dentropy, "dentropy", f32, rows)
     dev = _device_of(logits, lse, dlogits, targets, dlogp, entropy, dentropy, status)
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = _raw_stream(dev)
     if status is None:
         status = _status_on(dev, stream)
-    _call(dev, (_lib or load_library()).gpt2k_token_logprobs_bwd, code, px, rows, V, ld, temperature, pt, pl, pg, pe,
+    _call(dev, _lib.gpt2k_token_logprobs_bwd, code, px, rows, V, ld, temperature, pt, pl, pg, pe,
           ph, pd, ldd, status.data_ptr(), stream)
     return status
