@@ -73,6 +73,11 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// Barrier `id` (1 .. 15) among `threads` threads of the CTA.
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // ------------------------------------------------------------------------ TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
@@ -348,39 +353,11 @@ __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t addr, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(addr), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// mbar_wait on a barrier of this CTA that threads of the other one arrive on too.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile uint32_t* abort,
-                                                  unsigned* status) {
-    const uint32_t addr = smem_u32(bar);
-    unsigned long long t0 = 0;
-    for (uint32_t it = 0;; ++it) {
-        if (mbar_try_wait_cluster(addr, parity)) return true;
-        if ((it & 255u) == 255u) {
-            if (*abort) return false;
-            const unsigned long long now = globaltimer();
-            if (t0 == 0) {
-                t0 = now;
-            } else if (now - t0 > WAIT_LIMIT_NS) {
-                *abort = 1u;
-                atomicOr(status, STATUS_TIMEOUT);
-                return false;
-            }
-        }
-    }
+// Arrival on another CTA's barrier. What it orders here is tensor memory (by the tcgen05 fences
+// around it), so the default scope does; .release.cluster, and .acquire.cluster at the wait, cost
+// some 3,000 and 300 cycles a tile (measured: they wait for and invalidate unrelated memory traffic).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // tma_load_2d into this CTA that completes its bytes on a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m, int x, int y, uint32_t bar) {

@@ -520,15 +520,9 @@ def _status_on(dev, stream):
         return _torch.zeros(1, dtype=_torch.int32, device=dev)
 
 
-def _call(dev, fn, *args):
-    """fn(*args) with device dev current; raises on an error code."""
-    if _current_device() == dev:
-        rc = fn(*args)
-    else:
-        with _torch.cuda.device(dev):
-            rc = fn(*args)
-    if rc != GPT2_OK:
-        _check(rc)
+def _on_device(dev, fn, args):
+    with _torch.cuda.device(dev):
+        return fn(*args)
 
 
 def quantize_rows(x, q, scale, stream=None):
@@ -540,7 +534,10 @@ def quantize_rows(x, q, scale, stream=None):
     dev = _device_of(x, q, scale)
     if stream is None:
         stream = _raw_stream(dev)
-    _call(dev, _lib.gpt2k_quantize_rows, code, px, rows, K, ldx, pq, ldq, ps, stream)
+    args = (code, px, rows, K, ldx, pq, ldq, ps, stream)
+    rc = _lib.gpt2k_quantize_rows(*args) if _current_device() == dev else _on_device(dev, _lib.gpt2k_quantize_rows, args)
+    if rc:
+        _check(rc)
 
 
 def matmul_i8(A, a_scale, B, b_scale, out, epilogue: str = "store", bias=None, resid=None, status=None, stream=None):
@@ -563,8 +560,10 @@ def matmul_i8(A, a_scale, B, b_scale, out, epilogue: str = "store", bias=None, r
         stream = _raw_stream(dev)
     if status is None:
         status = _status_on(dev, stream)
-    _call(dev, _lib.gpt2k_matmul_i8, pa, lda, psa, pb, ldb, psb, M, N, K, EPILOGUE[epilogue],
-          code, po, ldo, pbias, pr, ldr, status.data_ptr(), stream)
+    args = (pa, lda, psa, pb, ldb, psb, M, N, K, EPILOGUE[epilogue], code, po, ldo, pbias, pr, ldr, status.data_ptr(), stream)
+    rc = _lib.gpt2k_matmul_i8(*args) if _current_device() == dev else _on_device(dev, _lib.gpt2k_matmul_i8, args)
+    if rc:
+        _check(rc)
     return status
 
 
@@ -587,8 +586,10 @@ def token_logprobs(logits, V: int, temperature: float, targets=None, logp=None, 
         stream = _raw_stream(dev)
     if status is None:
         status = _status_on(dev, stream)
-    _call(dev, _lib.gpt2k_token_logprobs, code, px, rows, V, ld, temperature, pt, k, pl, pe, ps,
-          pi, pp, status.data_ptr(), stream)
+    args = (code, px, rows, V, ld, temperature, pt, k, pl, pe, ps, pi, pp, status.data_ptr(), stream)
+    rc = _lib.gpt2k_token_logprobs(*args) if _current_device() == dev else _on_device(dev, _lib.gpt2k_token_logprobs, args)
+    if rc:
+        _check(rc)
     return status
 
 
@@ -612,6 +613,8 @@ def token_logprobs_bwd(logits, V: int, temperature: float, lse, dlogits, targets
         stream = _raw_stream(dev)
     if status is None:
         status = _status_on(dev, stream)
-    _call(dev, _lib.gpt2k_token_logprobs_bwd, code, px, rows, V, ld, temperature, pt, pl, pg, pe,
-          ph, pd, ldd, status.data_ptr(), stream)
+    args = (code, px, rows, V, ld, temperature, pt, pl, pg, pe, ph, pd, ldd, status.data_ptr(), stream)
+    rc = _lib.gpt2k_token_logprobs_bwd(*args) if _current_device() == dev else _on_device(dev, _lib.gpt2k_token_logprobs_bwd, args)
+    if rc:
+        _check(rc)
     return status
