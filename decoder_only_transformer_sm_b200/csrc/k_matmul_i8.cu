@@ -12,6 +12,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "kernels.cuh"
 #include "tc_ptx.cuh"
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(Tile<BN, CTAS>::THREADS, 1)
             tc::mbar_wait(&ctl->drain, 0, &no_abort, status);
         }
     } else {
-        constexpr int FULL = 128 / (int)sizeof(O), CW = L::WCOLS < FULL ? L::WCOLS : FULL;   // columns of a chunk
+        constexpr int CW = 128 / (int)sizeof(O);   // columns of a chunk
         constexpr int PER = 16 / sizeof(O);
         const bool tma_out = grid.tma_out;
         const int ew = warp - 2, quarter = warp & 3, cbase = (ew >> 2) * L::WCOLS;
@@ -618,7 +619,7 @@ bool whole_segments(const void* p, long long ld, int es) { return ((uintptr_t)p 
 template <int KIND, typename O, int BN, int CTAS>
 bool launch_tc(const Ctx& ctx, const I8Product& p) {
     using L = Tile<BN, CTAS>;
-    constexpr int FULL = 128 / (int)sizeof(O), CW = L::WCOLS < FULL ? L::WCOLS : FULL;
+    constexpr int CW = 128 / (int)sizeof(O);
     CUtensorMap ta, tb, to;
     const CUtensorMapDataType I8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     TileGrid g;
@@ -634,7 +635,7 @@ bool launch_tc(const Ctx& ctx, const I8Product& p) {
         return false;
     // TMA stores are asynchronous, but their bursts hold up the operands' loads: they pay for fp32 results
     // and short sums (16384 x 2304 in bf16: K = 128 21 us against 27 with plain stores, K = 768 35.6 against 33.4).
-    g.tma_out = g.vec_out && CW * sizeof(O) == 128 && (sizeof(O) == 4 || g.k_blocks <= 4);
+    g.tma_out = g.vec_out && (sizeof(O) == 4 || g.k_blocks <= 4);
     if (g.tma_out) {
         if (!make_map(&to, sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                       sizeof(O), p.out, p.M, p.N, p.ldo, CW, 32))
@@ -670,14 +671,21 @@ bool launch_kind(const Ctx& ctx, const I8Product& p) {
             else launch_rows<KIND, O, 8>(ctx, p);
             return true;
         }
-        // the widest tile that still gives (nearly) every SM one
-        auto fills = [&](int bm, int bn, int units) {
-            return 8ll * ceil_div(p.M, bm) * ceil_div(p.N, bn) >= 7ll * units;
+        // The tile width by its time: a start, then for each round of tiles over the SMs the K blocks and what
+        // of the epilogue the next tile's products do not cover. One MMA takes its issuing thread 120-170 cycles
+        // whatever its width, so a K block costs narrow tiles hardly less; they win while they fill SMs that wide
+        // ones leave idle. (us, measured with both operands in L2 over 64 .. 4096 rows: 64 x 2304 x 768 5.0 with
+        // 64 columns, 5.2 with 128, 7.2 with a pair; 1024 x 2304 x 768 7.4, 5.9, 8.2; 256 x 50304 x 768 26.8, 18.4, 14.2.)
+        const int kb = ceil_div(p.K, 128);
+        auto time = [&](int bm, int bn, int units, float start, float block, float tile) {
+            const float tiles = (float)ceil_div(p.M, bm) * (float)ceil_div(p.N, bn);
+            return start + ceilf(tiles / units) * (kb * block + tile);
         };
-        if (fills(256, 256, ctx.num_sms / 2)) return launch_tc<KIND, O, 256, 2>(ctx, p);
-        if (fills(128, 128, ctx.num_sms)) return launch_tc<KIND, O, 128, 1>(ctx, p);
-        if (fills(128, 64, ctx.num_sms)) return launch_tc<KIND, O, 64, 1>(ctx, p);
-        return launch_tc<KIND, O, 32, 1>(ctx, p);
+        const float t256 = time(256, 256, ctx.num_sms / 2, 3.9f, 0.36f, 1.1f);
+        const float t128 = time(128, 128, ctx.num_sms, 2.6f, 0.32f, 0.7f);
+        const float t64 = time(128, 64, ctx.num_sms, 2.5f, 0.30f, 0.6f);
+        if (t256 <= t128 && t256 <= t64) return launch_tc<KIND, O, 256, 2>(ctx, p);
+        return t128 <= t64 ? launch_tc<KIND, O, 128, 1>(ctx, p) : launch_tc<KIND, O, 64, 1>(ctx, p);
     }
     const long long tiles = (long long)ceil_div(p.N, ST) * ceil_div(p.M, ST);
     matmul_i8_simt_kernel<KIND, O><<<(unsigned)tiles, 256, 0, ctx.stream>>>(p);

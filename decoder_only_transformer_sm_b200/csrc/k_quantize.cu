@@ -15,7 +15,8 @@
 // (up to 8 a thread) between the maximum and the codes. Rows may start at
 // any element and codes at any byte: the elements before a row's first 16-byte boundary
 // and after its last one are held one a thread, and the codes go through shared memory,
-// laid out there like the memory they go to, so that they leave in 16-byte stores too.
+// laid out there like the memory they go to, so that they leave in 16-byte stores too. Where
+// rows and codes are whole vectors (ALIGNED) none of that is needed: the codes go straight out.
 #include "kernels.cuh"
 
 namespace gpt2 {
@@ -104,10 +105,13 @@ __device__ __forceinline__ void unpack(const uint4& q, float (&f)[4], float) {
     f[2] = __uint_as_float(q.z);
     f[3] = __uint_as_float(q.w);
 }
-// Largest magnitude of a vector: two 16-bit ones at a time for bf16 (`m` in both halves).
+// Largest magnitude of a vector, NaN above all: two at a time for bf16 (`m` in both halves).
 __device__ __forceinline__ unsigned larger(unsigned m, const uint4& q, bf16) {
-    constexpr unsigned K2 = 0x7fff7fffu;
-    return __vmaxu2(__vmaxu2(m, __vmaxu2(q.x & K2, q.y & K2)), __vmaxu2(q.z & K2, q.w & K2));
+    const unsigned u[4] = {q.x, q.y, q.z, q.w};
+    __nv_bfloat162 r = *reinterpret_cast<const __nv_bfloat162*>(&m);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r = __hmax2_nan(r, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u[i])));
+    return *reinterpret_cast<const unsigned*>(&r);
 }
 __device__ __forceinline__ unsigned larger(unsigned m, const uint4& q, float) {
     constexpr unsigned K1 = 0x7fffffffu;
@@ -119,7 +123,7 @@ __device__ __forceinline__ unsigned whole(unsigned m, float) { return m; }
 constexpr int QV = 8;   // vectors a thread
 
 // G threads a row, QT a block.
-template <typename T, int G, int QT>
+template <typename T, int G, int QT, bool ALIGNED>
 __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* __restrict__ x, long long ldx, int rows, int K,
                                                            int8_t* __restrict__ q, long long ldq,
                                                            float* __restrict__ scale) {
@@ -131,8 +135,8 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
     const bool live = row < rows;
     const T* xr = x + (live ? row : 0) * ldx;
     int8_t* qr = q + (live ? row : 0) * ldq;
-    const int head = min(K, (int)((16 - ((uintptr_t)xr & 15)) & 15) / (int)sizeof(T));
-    const int full = (K - head) / N, tail = K - head - full * N;
+    const int head = ALIGNED ? 0 : min(K, (int)((16 - ((uintptr_t)xr & 15)) & 15) / (int)sizeof(T));
+    const int full = (K - head) / N, tail = ALIGNED ? 0 : K - head - full * N;
     // this thread's vectors, and its element of the head and of the tail
     uint4 v[QV];
     float h = 0.f, e = 0.f;
@@ -141,8 +145,8 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
 #pragma unroll
         for (int i = 0; i < QV; ++i)
             v[i] = t + i * G < full ? __ldg(reinterpret_cast<const uint4*>(xr + head) + t + i * G) : make_uint4(0, 0, 0, 0);
-        if (t < head) h = to_f(xr[t]);
-        if (t < tail) e = to_f(xr[K - tail + t]);
+        if (!ALIGNED && t < head) h = to_f(xr[t]);
+        if (!ALIGNED && t < tail) e = to_f(xr[K - tail + t]);
 #pragma unroll
         for (int i = 0; i < QV; ++i) m = larger(m, v[i], T());
         m = max(whole(m, T()), max(magnitude(h), magnitude(e)));
@@ -158,6 +162,21 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
     const bool fine = m < 0x7f800000u;
     if (live && t == 0) scale[row] = fine ? __uint_as_float(m) / 127.f : __uint_as_float(0x7fc00000u);
     const float a = fine ? __uint_as_float(m) : 0.f, inv = inverse(a);
+    if (ALIGNED) {
+        if (!live) return;
+#pragma unroll
+        for (int i = 0; i < QV; ++i) {
+            if (t + i * G < full) {
+                float f[N];
+                unsigned c[N / 4];
+                unpack(v[i], f, T());
+                codes<N>(f, a, inv, c);
+                if (N == 8) *reinterpret_cast<uint2*>(qr + (t + i * G) * N) = make_uint2(c[0], c[N / 4 - 1]);
+                else *reinterpret_cast<unsigned*>(qr + (t + i * G) * N) = c[0];
+            }
+        }
+        return;
+    }
     const int lead = (int)((uintptr_t)qr & 15);
     int8_t* room = reinterpret_cast<int8_t*>(staged) + in_block * ((K + 15 + 16 + 15) / 16 * 16) + lead;
     if (live) {
@@ -198,8 +217,14 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
 
 template <typename T, int G, int QT = (G > 128 ? G : 128)>
 void launch_short(const Ctx& ctx, const T* x, long long ldx, int rows, int K, int8_t* q, long long ldq, float* scale) {
-    const size_t room = (size_t)(QT / G) * ((K + 15 + 16 + 15) / 16 * 16);
-    quantize_rows_kernel<T, G, QT><<<ceil_div(rows, QT / G), QT, room, ctx.stream>>>(x, ldx, rows, K, q, ldq, scale);
+    constexpr int N = 16 / sizeof(T);
+    const bool aligned = ((uintptr_t)x & 15) == 0 && ((uintptr_t)q & (N - 1)) == 0 && (ldx | ldq | K) % N == 0;
+    const int grid = ceil_div(rows, QT / G);
+    if (aligned)
+        quantize_rows_kernel<T, G, QT, true><<<grid, QT, 0, ctx.stream>>>(x, ldx, rows, K, q, ldq, scale);
+    else
+        quantize_rows_kernel<T, G, QT, false><<<grid, QT, (QT / G) * ((K + 15 + 16 + 15) / 16 * 16), ctx.stream>>>(
+            x, ldx, rows, K, q, ldq, scale);
 }
 
 }  // namespace

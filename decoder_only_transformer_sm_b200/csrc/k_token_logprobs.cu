@@ -32,6 +32,7 @@ typedef unsigned long long u64;
 
 constexpr float NEG_INF = -__builtin_huge_valf();
 constexpr float LOWEST = -3.402823466e38f;
+constexpr float MASK = -1e30f;
 constexpr float LOG2E = 1.4426950408889634f;
 __device__ __forceinline__ float nan_value() { return __uint_as_float(0x7fc00000u); }
 
@@ -130,34 +131,48 @@ __device__ __forceinline__ uint4 load_vec(const T* row, const RowVecs<T>& rv, in
     return gather_vec(row, rv, i, end);
 }
 
-// Largest and smallest of U vectors, NaN passed over.
+// Largest of U vectors, NaN passed over.
 template <int U>
-__device__ __forceinline__ void extremes(const uint4 (&q)[U], float& top, float& low, bf16) {
-    __nv_bfloat162 hi, lo;
+__device__ __forceinline__ float largest_of(const uint4 (&q)[U], bf16) {
+    __nv_bfloat162 hi;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q[u]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            hi = u + j ? __hmax2(hi, h[j]) : h[j];
-            lo = u + j ? __hmin2(lo, h[j]) : h[j];
-        }
+        for (int j = 0; j < 4; ++j) hi = u + j ? __hmax2(hi, h[j]) : h[j];
     }
-    const float2 a = __bfloat1622float2(hi), b = __bfloat1622float2(lo);
-    top = fmaxf(a.x, a.y);
-    low = fminf(b.x, b.y);
+    const float2 a = __bfloat1622float2(hi);
+    return fmaxf(a.x, a.y);
 }
 template <int U>
-__device__ __forceinline__ void extremes(const uint4 (&q)[U], float& top, float& low, float) {
-    top = NEG_INF;
-    low = -NEG_INF;
+__device__ __forceinline__ float largest_of(const uint4 (&q)[U], float) {
+    float top = NEG_INF;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         float f[4];
         unpack(q[u], f, 0.f);
         top = fmaxf(fmaxf(top, fmaxf(f[0], f[1])), fmaxf(f[2], f[3]));
-        low = fminf(fminf(low, fminf(f[0], f[1])), fminf(f[2], f[3]));
     }
+    return top;
+}
+// Values below `low` (a masked -inf) raised to it, NaN kept; two at a time for bf16.
+__device__ __forceinline__ uint4 floored(const uint4& q, float low, bf16) {
+    const __nv_bfloat162 l = __floats2bfloat162_rn(low, low);
+    uint4 r;
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
+    __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(&r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = __hmax2_nan(h[j], l);
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint4 floored(const uint4& q, float low, float) {
+    return make_uint4(__float_as_uint(max_nan(__uint_as_float(q.x), low)), __float_as_uint(max_nan(__uint_as_float(q.y), low)),
+                      __float_as_uint(max_nan(__uint_as_float(q.z), low)), __float_as_uint(max_nan(__uint_as_float(q.w), low)));
 }
 
 struct Sums {
@@ -175,8 +190,9 @@ struct Sums {
         s += o.s;
         w += o.w;
     }
-    // The terms of U vectors, none above m. MASKED: there may be -inf, whose e = 0 meets d = -inf.
-    template <bool MASKED, typename T, int U>
+    // The terms of U vectors, none above m and one at least above MASK, so m > MASK too: raised
+    // to MASK a masked value still has e = 0, and a finite d.
+    template <typename T, int U>
     __device__ __forceinline__ void add(const uint4 (&q)[U], float c) {
         constexpr int N = RowVecs<T>::N;
         const f32x2 m2 = pk2(-m, -m), c2 = pk2(c, c);
@@ -184,18 +200,13 @@ struct Sums {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float f[N];
-            unpack(q[u], f, T());
+            unpack(floored(q[u], MASK, T()), f, T());
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
-                f32x2 d2 = add2(pk2(f[j], f[j + 1]), m2);
+                const f32x2 d2 = add2(pk2(f[j], f[j + 1]), m2);
                 float y0, y1;
                 upk2(mul2(d2, c2), y0, y1);
                 const f32x2 e2 = pk2(ex2_approx(y0), ex2_approx(y1));
-                if (MASKED) {
-                    float d0, d1;
-                    upk2(d2, d0, d1);
-                    d2 = pk2(fmaxf(d0, LOWEST), fmaxf(d1, LOWEST));
-                }
                 s2 = add2(s2, e2);
                 w2 = fma2(e2, d2, w2);
             }
@@ -205,6 +216,20 @@ struct Sums {
         upk2(w2, w0, w1);
         s = s0 + s1;
         w = w0 + w1;
+    }
+    // A vector whose largest value is -inf or near the type's lowest (or that holds NaN alone).
+    template <typename T>
+    __device__ __noinline__ void add_lowest(uint4 q, float top, float c) {
+        constexpr int N = RowVecs<T>::N;
+        if (top > m) raise(top, c);
+        float f[N];
+        unpack(q, f, T());
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float d = f[j] - m, e = ex2_approx(d * c);
+            s += e;
+            w += e * fmaxf(d, LOWEST);   // a masked value has e = 0 and d = -inf
+        }
     }
 };
 
@@ -251,10 +276,10 @@ __device__ __forceinline__ void for_top(const u64* keys, int n, int k, int nt, F
 }
 
 // Leaves in sm.cand (sm.n_cand of them, visible to the block) keys among which are the
-// block's top_k.
+// block's top_k. any_nan: the block's part holds NaN or +inf.
 template <typename T, int NT>
 __device__ __forceinline__ void top_of_block(ForwardSmem<NT>& sm, const T* x, const RowVecs<T>& rv, int begin, int end,
-                                             int top_k) {
+                                             int top_k, bool any_nan) {
     constexpr int N = RowVecs<T>::N, GROUP = GROUP_OF<NT>;
     const int tid = threadIdx.x, lane = tid & 31;
     if (tid < 64) {
@@ -275,33 +300,31 @@ __device__ __forceinline__ void top_of_block(ForwardSmem<NT>& sm, const T* x, co
     const float bound_value = value_of(bound);
     const int steps = ceil_div(end - begin, NT), n_again = sm.n_again;
     if (n_again <= 2 * top_k) {
-        // a thread takes single vectors of all the groups
+        // a thread takes single vectors of R groups at a time
         constexpr int R = 4;
-        for (int k0 = tid; k0 < n_again * steps * GROUP; k0 += R * NT) {
-            uint4 q[R];
-            int at[R];
+        for (int g0 = 0; g0 < n_again; g0 += R) {
+            for (int k = tid; k < steps * GROUP; k += NT) {
+                uint4 q[R];
+                int at[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int k = k0 + r * NT, step = k / GROUP % steps, g = k / GROUP / steps;
-                at[r] = g < n_again ? begin + step * NT + sm.again[g] + k % GROUP : end;
-                q[r] = load_vec(x, rv, at[r], end);
-            }
+                for (int r = 0; r < R; ++r) {
+                    at[r] = g0 + r < n_again ? begin + k / GROUP * NT + sm.again[g0 + r] + k % GROUP : end;
+                    q[r] = load_vec(x, rv, at[r], end);
+                }
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if (at[r] >= end) continue;
-                float f[N];
-                unpack(q[r], f, T());
-                bool pass = false;
+                for (int r = 0; r < R; ++r) {
+                    const uint4 one[1] = {q[r]};
+                    if (at[r] >= end || (largest_of(one, T()) < bound_value && !any_nan)) continue;
+                    float f[N];
+                    unpack(q[r], f, T());
+                    const int first = rv.first(at[r]), last = rv.last(at[r]);
 #pragma unroll
-                for (int j = 0; j < N; ++j) pass |= !(f[j] < bound_value);
-                if (!pass) continue;
-                const int first = rv.first(at[r]), last = rv.last(at[r]);
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const unsigned o = order_of(f[j]);
-                    if (o >= bound && first + j < last) {
-                        const int n = atomicAdd(&sm.n_cand, 1);
-                        if (n < NT) sm.cand[n] = key_of(o, first + j);
+                    for (int j = 0; j < N; ++j) {
+                        const unsigned o = order_of(f[j]);
+                        if (o >= bound && first + j < last) {
+                            const int n = atomicAdd(&sm.n_cand, 1);
+                            if (n < NT) sm.cand[n] = key_of(o, first + j);
+                        }
                     }
                 }
             }
@@ -374,44 +397,39 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const T* __restrict_
 
     Sums a = {LOWEST, 0.f, 0.f};
     float largest = NEG_INF;
-    auto take = [&](const auto& q) {
-        float top, low;
-        extremes(q, top, low, T());
+    auto take = [&](const uint4 (&q)[U]) {
+        const float top = largest_of(q, T());
         largest = fmaxf(largest, top);
-        if (top > a.m) a.raise(top, c);
-        if (low > -1e30f) a.add<false, T>(q, c);
-        else a.add<true, T>(q, c);
+        if (top > MASK) {
+            if (top > a.m) a.raise(top, c);
+            a.add<T>(q, c);
+        } else {
+            for (int u = 0; u < U; ++u) a.add_lowest<T>(q[u], top, c);
+        }
     };
-    int i = begin + tid;
-    {
-        // batches of U whole vectors, the next one's loads under way
-        const uint4* at = reinterpret_cast<const uint4*>(x + rv.head);
-        const int stop = min(end, rv.full) - (U - 1) * NT;
-        uint4 q[U];
-        if (i < stop) {
+    // batches of U vectors; the next one's loads are under way while one is taken
+    auto load = [&](uint4 (&q)[U], int i) {
+        if (i + (U - 1) * NT < min(end, rv.full)) {
+            const uint4* at = reinterpret_cast<const uint4*>(x + rv.head) + i;
 #pragma unroll
-            for (int u = 0; u < U; ++u) q[u] = __ldg(at + i + u * NT);
-        }
-        for (; i < stop; i += U * NT) {
-            uint4 next[U];
-            if (i + U * NT < stop) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) next[u] = __ldg(at + i + (U + u) * NT);
-            }
-            take(q);
-#pragma unroll
-            for (int u = 0; u < U; ++u) q[u] = next[u];
-        }
-        // what is left: fewer than U vectors, and the row's ends
-        if (i < end) {
+            for (int u = 0; u < U; ++u) q[u] = __ldg(at + u * NT);
+        } else if (i < end) {
 #pragma unroll
             for (int u = 0; u < U; ++u) q[u] = load_vec(x, rv, i + u * NT, end);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (i + u * NT >= end) break;
-                const uint4 one[1] = {q[u]};
-                take(one);
-            }
+        }
+    };
+    {
+        uint4 q[U], next[U];
+        int i = begin + tid;
+        load(q, i);
+        while (i < end) {
+            load(next, i + U * NT);
+            take(q);
+            i += U * NT;
+            if (i >= end) break;
+            load(q, i + U * NT);
+            take(next);
+            i += U * NT;
         }
     }
 
@@ -450,7 +468,7 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const T* __restrict_
             a.w += sm.sums[w].w;
         }
     }
-    if (out.top_k && (CLUSTER || a.s != 0.f)) top_of_block<T, NT>(sm, x, rv, begin, end, out.top_k);
+    if (out.top_k && (CLUSTER || a.s != 0.f)) top_of_block<T, NT>(sm, x, rv, begin, end, out.top_k, a.s != a.s);
     const u64* keys = sm.cand;
     int n_keys = sm.n_cand;
     if (CLUSTER) {
