@@ -9,16 +9,15 @@
 // w. A row of which nothing is left has lse = log p = -inf and H = 0; a row with NaN or
 // +inf has NaN in all of them.
 //
-// Forward: one pass over the row. A thread keeps a running (m, s, w) and rescales
-// it when a load of several vectors raises m; the block's threads, and with few rows
-// the blocks of a cluster (distributed shared memory), join theirs at the end.
-// Top alternatives come from the same pass: neighbouring threads share one of 64 groups,
-// whose largest value is known at the end. A group is read again (from L2) only if
-// fewer than top_k groups have a larger maximum: no other group can hold one of the
-// top_k, and the smallest maximum of those read again is a bound that few other values
-// pass. What passes it is ranked by 64-bit keys (value, then lowest index). Where more
-// values pass than there is room for (many equal ones), each warp instead keeps a sorted list while it
-// reads its own groups again.
+// Forward: one pass over the row by NT threads (a warp for short rows, a block, or with
+// few long rows the blocks of a cluster). A thread keeps a running (m, s, w) and rescales it
+// when a load of several vectors raises m; the threads join theirs at the end, the blocks
+// through distributed shared memory. Top alternatives come from the same pass: a thread
+// knows its largest value at the end, and the top_k-th largest of those is a bound that
+// at least top_k values of the row reach. Only threads that reach it can hold one of the
+// top_k: what they read is read again (from L2), and the few values that reach the bound
+// are ranked by 64-bit keys (value, then lowest index). Where more reach it than there is
+// room for (many equal ones), each warp instead keeps a sorted list while it reads again.
 #include <cooperative_groups.h>
 
 #include "kernels.cuh"
@@ -32,7 +31,6 @@ typedef unsigned long long u64;
 
 constexpr float NEG_INF = -__builtin_huge_valf();
 constexpr float LOWEST = -3.402823466e38f;
-constexpr float MASK = -1e30f;
 constexpr float LOG2E = 1.4426950408889634f;
 __device__ __forceinline__ float nan_value() { return __uint_as_float(0x7fc00000u); }
 
@@ -131,48 +129,34 @@ __device__ __forceinline__ uint4 load_vec(const T* row, const RowVecs<T>& rv, in
     return gather_vec(row, rv, i, end);
 }
 
-// Largest of U vectors, NaN passed over.
+// Largest and smallest of U vectors, NaN passed over.
 template <int U>
-__device__ __forceinline__ float largest_of(const uint4 (&q)[U], bf16) {
-    __nv_bfloat162 hi;
+__device__ __forceinline__ void extremes(const uint4 (&q)[U], float& top, float& low, bf16) {
+    __nv_bfloat162 hi, lo;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q[u]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) hi = u + j ? __hmax2(hi, h[j]) : h[j];
+        for (int j = 0; j < 4; ++j) {
+            hi = u + j ? __hmax2(hi, h[j]) : h[j];
+            lo = u + j ? __hmin2(lo, h[j]) : h[j];
+        }
     }
-    const float2 a = __bfloat1622float2(hi);
-    return fmaxf(a.x, a.y);
+    const float2 a = __bfloat1622float2(hi), b = __bfloat1622float2(lo);
+    top = fmaxf(a.x, a.y);
+    low = fminf(b.x, b.y);
 }
 template <int U>
-__device__ __forceinline__ float largest_of(const uint4 (&q)[U], float) {
-    float top = NEG_INF;
+__device__ __forceinline__ void extremes(const uint4 (&q)[U], float& top, float& low, float) {
+    top = NEG_INF;
+    low = -NEG_INF;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         float f[4];
         unpack(q[u], f, 0.f);
         top = fmaxf(fmaxf(top, fmaxf(f[0], f[1])), fmaxf(f[2], f[3]));
+        low = fminf(fminf(low, fminf(f[0], f[1])), fminf(f[2], f[3]));
     }
-    return top;
-}
-// Values below `low` (a masked -inf) raised to it, NaN kept; two at a time for bf16.
-__device__ __forceinline__ uint4 floored(const uint4& q, float low, bf16) {
-    const __nv_bfloat162 l = __floats2bfloat162_rn(low, low);
-    uint4 r;
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
-    __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(&r);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = __hmax2_nan(h[j], l);
-    return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ uint4 floored(const uint4& q, float low, float) {
-    return make_uint4(__float_as_uint(max_nan(__uint_as_float(q.x), low)), __float_as_uint(max_nan(__uint_as_float(q.y), low)),
-                      __float_as_uint(max_nan(__uint_as_float(q.z), low)), __float_as_uint(max_nan(__uint_as_float(q.w), low)));
 }
 
 struct Sums {
@@ -190,9 +174,8 @@ struct Sums {
         s += o.s;
         w += o.w;
     }
-    // The terms of U vectors, none above m and one at least above MASK, so m > MASK too: raised
-    // to MASK a masked value still has e = 0, and a finite d.
-    template <typename T, int U>
+    // The terms of U vectors, none above m. MASKED: there may be -inf, whose e = 0 meets d = -inf.
+    template <bool MASKED, typename T, int U>
     __device__ __forceinline__ void add(const uint4 (&q)[U], float c) {
         constexpr int N = RowVecs<T>::N;
         const f32x2 m2 = pk2(-m, -m), c2 = pk2(c, c);
@@ -200,13 +183,18 @@ struct Sums {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float f[N];
-            unpack(floored(q[u], MASK, T()), f, T());
+            unpack(q[u], f, T());
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
-                const f32x2 d2 = add2(pk2(f[j], f[j + 1]), m2);
+                f32x2 d2 = add2(pk2(f[j], f[j + 1]), m2);
                 float y0, y1;
                 upk2(mul2(d2, c2), y0, y1);
                 const f32x2 e2 = pk2(ex2_approx(y0), ex2_approx(y1));
+                if (MASKED) {
+                    float d0, d1;
+                    upk2(d2, d0, d1);
+                    d2 = pk2(fmaxf(d0, LOWEST), fmaxf(d1, LOWEST));
+                }
                 s2 = add2(s2, e2);
                 w2 = fma2(e2, d2, w2);
             }
@@ -216,20 +204,6 @@ struct Sums {
         upk2(w2, w0, w1);
         s = s0 + s1;
         w = w0 + w1;
-    }
-    // A vector whose largest value is -inf or near the type's lowest (or that holds NaN alone).
-    template <typename T>
-    __device__ __noinline__ void add_lowest(uint4 q, float top, float c) {
-        constexpr int N = RowVecs<T>::N;
-        if (top > m) raise(top, c);
-        float f[N];
-        unpack(q, f, T());
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float d = f[j] - m, e = ex2_approx(d * c);
-            s += e;
-            w += e * fmaxf(d, LOWEST);   // a masked value has e = 0 and d = -inf
-        }
     }
 };
 
@@ -246,27 +220,34 @@ __device__ __forceinline__ void insert(u64& list, u64 key, bool pass) {
     }
 }
 
-// Neighbouring threads of a group, for 64 groups a block.
+// All threads of a row meet (NT = 32: a warp, several rows a block).
 template <int NT>
-constexpr int GROUP_OF = NT / 64;
+__device__ __forceinline__ void meet() {
+    if (NT == 32) __syncwarp();
+    else __syncthreads();
+}
 
 template <int NT>
 struct ForwardSmem {
-    alignas(16) unsigned group[64];       // order of each group's largest value
-    u64 cand[NT];                         // the warps' lists, packed
+    alignas(16) unsigned largest[NT];     // order of each thread's largest value
+    static constexpr int ROOM = NT < 128 ? 96 : 192;
+    u64 cand[ROOM];                       // keys that reach the bound (the warps' lists: NT at most)
     Sums sums[NT / 32];
-    int again[64];                        // first threads of the groups to read again
+    int again[NT];                        // the threads whose values are read again
     unsigned bound;
     int n_cand, n_again;
-    // of the cluster's first block: every block's results
-    Sums all_sums[8];
-    u64 all_top[8 * LOGPROB_MAX_TOP];
+};
+
+// Of a cluster's first block: every block's results.
+struct ClusterSmem {
+    Sums sums[8];
+    u64 top[8 * LOGPROB_MAX_TOP];
 };
 
 // Ranks n keys in shared memory; rank(i, key) is called for those among the k largest.
 template <typename F>
 __device__ __forceinline__ void for_top(const u64* keys, int n, int k, int nt, F rank) {
-    for (int i = threadIdx.x; i < n; i += nt) {
+    for (int i = threadIdx.x % nt; i < n; i += nt) {
         const u64 mine = keys[i];
         if (mine == 0) continue;
         int above = 0;
@@ -275,79 +256,109 @@ __device__ __forceinline__ void for_top(const u64* keys, int n, int k, int nt, F
     }
 }
 
-// Leaves in sm.cand (sm.n_cand of them, visible to the block) keys among which are the
-// block's top_k. any_nan: the block's part holds NaN or +inf.
+// Alternatives up to which a warp finds the bound by walking down from the largest value.
+constexpr int WALK = 8;
+
+// Leaves in sm.cand (sm.n_cand of them, visible to the threads of the row) keys among which
+// are the largest top_k of the vectors begin .. end - 1. any_nan: there is NaN or +inf.
 template <typename T, int NT>
-__device__ __forceinline__ void top_of_block(ForwardSmem<NT>& sm, const T* x, const RowVecs<T>& rv, int begin, int end,
-                                             int top_k, bool any_nan) {
-    constexpr int N = RowVecs<T>::N, GROUP = GROUP_OF<NT>;
-    const int tid = threadIdx.x, lane = tid & 31;
-    if (tid < 64) {
-        const unsigned order = sm.group[tid];
-        int above = 0;
+__device__ __forceinline__ void find_top(ForwardSmem<NT>& sm, const T* x, const RowVecs<T>& rv, int begin, int end,
+                                         int top_k, bool any_nan) {
+    constexpr int N = RowVecs<T>::N, PER = NT / 32;
+    const int tid = threadIdx.x % NT, lane = tid & 31, warp = tid >> 5;
+    if (top_k <= WALK || NT == 32) {
+        if (warp == 0) {
+            unsigned key[PER], bound = 0xffffffffu;
 #pragma unroll
-        for (int j = 0; j < 64; j += 4) {
-            const uint4 g = *reinterpret_cast<const uint4*>(sm.group + j);
-            above += (g.x > order) + (g.y > order) + (g.z > order) + (g.w > order);
+            for (int i = 0; i < PER; ++i) key[i] = sm.largest[lane + 32 * i];
+            // distinct values from the largest on, until top_k threads have reached them
+            for (int n = 0; n < top_k && bound != 0;) {
+                unsigned below = 0;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) below = max(below, key[i] < bound ? key[i] : 0u);
+                bound = __reduce_max_sync(0xffffffffu, below);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) n += __popc(__ballot_sync(0xffffffffu, key[i] == bound));
+            }
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const unsigned in = __ballot_sync(0xffffffffu, key[i] >= bound);
+                if ((in >> lane) & 1) sm.again[n + __popc(in & ((1u << lane) - 1))] = lane + 32 * i;
+                n += __popc(in);
+            }
+            if (lane == 0) {
+                sm.bound = bound;
+                sm.n_again = n;
+            }
+        }
+    } else {   // every thread counts those above its own
+        const unsigned mine = sm.largest[tid];
+        int above = 0;
+#pragma unroll 8
+        for (int j = 0; j < NT; j += 4) {
+            const uint4 g = *reinterpret_cast<const uint4*>(sm.largest + j);
+            above += (g.x > mine) + (g.y > mine) + (g.z > mine) + (g.w > mine);
         }
         if (above < top_k) {
-            atomicMin(&sm.bound, order);
-            sm.again[atomicAdd(&sm.n_again, 1)] = tid * GROUP;
+            atomicMin(&sm.bound, mine);
+            sm.again[atomicAdd(&sm.n_again, 1)] = tid;
         }
     }
-    __syncthreads();
+    meet<NT>();
     const unsigned bound = sm.bound;
-    const float bound_value = value_of(bound);
     const int steps = ceil_div(end - begin, NT), n_again = sm.n_again;
     if (n_again <= 2 * top_k) {
-        // a thread takes single vectors of R groups at a time
-        constexpr int R = 4;
-        for (int g0 = 0; g0 < n_again; g0 += R) {
-            for (int k = tid; k < steps * GROUP; k += NT) {
-                uint4 q[R];
-                int at[R];
+        const float bound_value = value_of(bound), per_step = 1.f / steps;
+        constexpr int R = 2;
+        for (int k0 = tid; k0 < n_again * steps; k0 += R * NT) {
+            uint4 q[R];
+            int at[R];
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    at[r] = g0 + r < n_again ? begin + k / GROUP * NT + sm.again[g0 + r] + k % GROUP : end;
-                    q[r] = load_vec(x, rv, at[r], end);
-                }
+            for (int r = 0; r < R; ++r) {
+                // vector k % steps of thread again[k / steps] (k + 1/2 is off a whole multiple by more than the
+                // product's rounding: k < 2^21)
+                const int k = k0 + r * NT, g = (int)((k + 0.5f) * per_step);
+                at[r] = g < n_again ? begin + (k - g * steps) * NT + sm.again[g] : end;
+                q[r] = at[r] < end ? load_vec(x, rv, at[r], end) : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const uint4 one[1] = {q[r]};
-                    if (at[r] >= end || (largest_of(one, T()) < bound_value && !any_nan)) continue;
-                    float f[N];
-                    unpack(q[r], f, T());
-                    const int first = rv.first(at[r]), last = rv.last(at[r]);
+            for (int r = 0; r < R; ++r) {
+                const uint4 one[1] = {q[r]};
+                float top, low;
+                extremes(one, top, low, T());
+                if (at[r] >= end || (top < bound_value && !any_nan)) continue;
+                float f[N];
+                unpack(q[r], f, T());
+                const int first = rv.first(at[r]), last = rv.last(at[r]);
 #pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        const unsigned o = order_of(f[j]);
-                        if (o >= bound && first + j < last) {
-                            const int n = atomicAdd(&sm.n_cand, 1);
-                            if (n < NT) sm.cand[n] = key_of(o, first + j);
-                        }
-                    }
+                for (int j = 0; j < N; ++j) {
+                    if (f[j] < bound_value || first + j >= last) continue;
+                    const unsigned o = order_of(f[j]);
+                    if (o < bound) continue;
+                    const int n = atomicAdd(&sm.n_cand, 1);
+                    if (n < sm.ROOM) sm.cand[n] = key_of(o, first + j);
                 }
             }
         }
-        __syncthreads();
-        if (sm.n_cand <= NT) return;
-        __syncthreads();
+        meet<NT>();
+        if (sm.n_cand <= sm.ROOM) return;
+        meet<NT>();
         if (tid == 0) sm.n_cand = 0;
-        __syncthreads();
+        meet<NT>();
     }
     u64 list = 0;
-    // 32 lanes read a group's vectors of STEPS steps
-    constexpr int STEPS = 32 / (GROUP * N);
-    for (int g = tid >> 5; g < 64; g += NT / 32) {
-        if (sm.group[g] < bound) continue;
-        const int mine = g * GROUP + (lane / N) % GROUP, j = lane % N;
+    // 32 lanes read a thread's vectors of STEPS steps
+    constexpr int STEPS = 32 / N;
+    for (int g = warp; g < n_again; g += PER) {
+        const int mine = sm.again[g], j = lane % N;
         constexpr int R = 8;
         for (int i0 = begin; i0 < end; i0 += R * STEPS * NT) {
             float v[R];
             int at[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int i = i0 + (r * STEPS + lane / (GROUP * N)) * NT + mine;
+                const int i = i0 + (r * STEPS + lane / N) * NT + mine;
                 at[r] = -1;
                 v[r] = 0.f;
                 if (i < end) {
@@ -358,7 +369,7 @@ __device__ __forceinline__ void top_of_block(ForwardSmem<NT>& sm, const T* x, co
                     }
                 }
             }
-#pragma unroll
+#pragma unroll 1
             for (int r = 0; r < R; ++r) {
                 const unsigned o = order_of(v[r]);
                 const u64 k = key_of(o, at[r]);
@@ -373,17 +384,25 @@ __device__ __forceinline__ void top_of_block(ForwardSmem<NT>& sm, const T* x, co
     if (lane == 0 && kept) base = atomicAdd(&sm.n_cand, __popc(kept));
     base = __shfl_sync(0xffffffffu, base, 0);
     if ((kept >> lane) & 1) sm.cand[base + __popc(kept & ((1u << lane) - 1))] = list;
-    __syncthreads();
+    meet<NT>();
 }
 
+// Threads of a block: rows of a warp share one.
+template <int NT>
+constexpr int BLOCK_OF = NT < 128 ? 128 : NT;
+
 template <typename T, int NT, bool CLUSTER>
-__global__ void __launch_bounds__(NT) token_logprobs_kernel(const T* __restrict__ logits, long long ld, int V,
-                                                            float inv_tau, const int* __restrict__ targets,
-                                                            LogprobOut out, int parts, unsigned* status) {
-    constexpr int U = 4, GROUP = GROUP_OF<NT>;
-    __shared__ ForwardSmem<NT> sm;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int row = CLUSTER ? blockIdx.x / parts : blockIdx.x, part = CLUSTER ? blockIdx.x % parts : 0;
+__global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* __restrict__ logits, long long ld,
+                                                                      int rows, int V, float inv_tau,
+                                                                      const int* __restrict__ targets, LogprobOut out,
+                                                                      int parts, unsigned* status) {
+    constexpr int U = 4, ROWS = BLOCK_OF<NT> / NT;
+    __shared__ ForwardSmem<NT> sms[ROWS];
+    ForwardSmem<NT>& sm = sms[threadIdx.x / NT];
+    const int tid = threadIdx.x % NT, lane = tid & 31;
+    const int row = CLUSTER ? blockIdx.x / parts : blockIdx.x * ROWS + threadIdx.x / NT;
+    const int part = CLUSTER ? blockIdx.x % parts : 0;
+    if (ROWS > 1 && row >= rows) return;
     const T* x = logits + (long long)row * ld;
     const RowVecs<T> rv(x, V);
     const int per = CLUSTER ? ceil_div(rv.count(), parts) : rv.count();
@@ -391,100 +410,105 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const T* __restrict_
     const float c = LOG2E * inv_tau;
     if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     if (tid == 0) {
-        sm.bound = 0xffffffffu;
         sm.n_cand = sm.n_again = 0;
+        sm.bound = 0xffffffffu;
     }
 
     Sums a = {LOWEST, 0.f, 0.f};
     float largest = NEG_INF;
-    auto take = [&](const uint4 (&q)[U]) {
-        const float top = largest_of(q, T());
-        largest = fmaxf(largest, top);
-        if (top > MASK) {
-            if (top > a.m) a.raise(top, c);
-            a.add<T>(q, c);
-        } else {
-            for (int u = 0; u < U; ++u) a.add_lowest<T>(q[u], top, c);
-        }
-    };
-    // batches of U vectors; the next one's loads are under way while one is taken
-    auto load = [&](uint4 (&q)[U], int i) {
-        if (i + (U - 1) * NT < min(end, rv.full)) {
-            const uint4* at = reinterpret_cast<const uint4*>(x + rv.head) + i;
+    {
+        // batches of U whole vectors, the next one's loads under way
+        int i = begin + tid;
+        const uint4* at = reinterpret_cast<const uint4*>(x + rv.head);
+        const int stop = min(end, rv.full) - (U - 1) * NT;
+        uint4 q[U];
+        if (i < stop) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) q[u] = __ldg(at + u * NT);
-        } else if (i < end) {
+            for (int u = 0; u < U; ++u) q[u] = __ldg(at + i + u * NT);
+        }
+        for (; i < stop; i += U * NT) {
+            uint4 next[U];
+            if (i + U * NT < stop) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) next[u] = __ldg(at + i + (U + u) * NT);
+            }
+            float top, low;
+            extremes(q, top, low, T());
+            largest = fmaxf(largest, top);
+            if (top > a.m) a.raise(top, c);
+            if (low > -1e30f) a.add<false, T>(q, c);
+            else a.add<true, T>(q, c);
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = next[u];
+        }
+        // what is left: fewer than U vectors, and the row's ends
+        if (i < end) {
 #pragma unroll
             for (int u = 0; u < U; ++u) q[u] = load_vec(x, rv, i + u * NT, end);
-        }
-    };
-    {
-        uint4 q[U], next[U];
-        int i = begin + tid;
-        load(q, i);
-        while (i < end) {
-            load(next, i + U * NT);
-            take(q);
-            i += U * NT;
-            if (i >= end) break;
-            load(q, i + U * NT);
-            take(next);
-            i += U * NT;
+            float top, low;
+            extremes(q, top, low, T());
+            largest = fmaxf(largest, top);
+            if (top > a.m) a.raise(top, c);
+            a.add<true, T>(q, c);
         }
     }
 
-    unsigned order = 0;   // of this thread's largest value, then of its group's
     if (out.top_k) {
-        if (begin + tid < end) order = order_of(largest);
+        unsigned order = begin + tid < end ? order_of(largest) : 0u;
         if (a.s != a.s) {   // a NaN, or +inf: find out which
             for (int i = begin + tid; i < end; i += NT)
                 for (int v = rv.first(i); v < rv.last(i); ++v) order = max(order, order_of(to_f(x[v])));
         }
-#pragma unroll
-        for (int o = 1; o < GROUP; o *= 2) order = max(order, __shfl_xor_sync(0xffffffffu, order, o));
-        if (tid % GROUP == 0) sm.group[tid / GROUP] = order;
+        sm.largest[tid] = order;
     }
-    // the block's maximum first, so that every thread rescales once
+    // the maximum of all first, so that every thread rescales once
     {
-        const float wm = warp_max(a.m);
-        if (lane == 0) sm.sums[tid >> 5].m = wm;
-        __syncthreads();
-        float m = sm.sums[0].m;
+        float m = warp_max(a.m);
+        if (NT > 32) {
+            if (lane == 0) sm.sums[tid >> 5].m = m;
+            __syncthreads();
+            m = sm.sums[0].m;
 #pragma unroll
-        for (int w = 1; w < NT / 32; ++w) m = fmaxf(m, sm.sums[w].m);
+            for (int w = 1; w < NT / 32; ++w) m = fmaxf(m, sm.sums[w].m);
+        }
         a.raise(m, c);
         a.s = warp_sum(a.s);
         a.w = warp_sum(a.w);
-        if (lane == 0) {
-            sm.sums[tid >> 5].s = a.s;
-            sm.sums[tid >> 5].w = a.w;
-        }
-        __syncthreads();
-        a.s = sm.sums[0].s;
-        a.w = sm.sums[0].w;
+        if (NT > 32) {
+            if (lane == 0) {
+                sm.sums[tid >> 5].s = a.s;
+                sm.sums[tid >> 5].w = a.w;
+            }
+            __syncthreads();
+            a.s = sm.sums[0].s;
+            a.w = sm.sums[0].w;
 #pragma unroll
-        for (int w = 1; w < NT / 32; ++w) {
-            a.s += sm.sums[w].s;
-            a.w += sm.sums[w].w;
+            for (int w = 1; w < NT / 32; ++w) {
+                a.s += sm.sums[w].s;
+                a.w += sm.sums[w].w;
+            }
+        } else {
+            __syncwarp();
         }
     }
-    if (out.top_k && (CLUSTER || a.s != 0.f)) top_of_block<T, NT>(sm, x, rv, begin, end, out.top_k, a.s != a.s);
+    if (out.top_k && (CLUSTER || a.s != 0.f)) find_top<T, NT>(sm, x, rv, begin, end, out.top_k, a.s != a.s);
     const u64* keys = sm.cand;
-    int n_keys = sm.n_cand;
-    if (CLUSTER) {
+    int n_keys = out.top_k ? sm.n_cand : 0;
+    if constexpr (CLUSTER) {
+        __shared__ ClusterSmem cs;
         auto cluster = cg::this_cluster();
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // every block has started
-        ForwardSmem<NT>* first = cluster.map_shared_rank(&sm, 0);
-        if (tid == 0) first->all_sums[part] = a;
+        ClusterSmem* first = cluster.map_shared_rank(&cs, 0);
+        if (tid == 0) first->sums[part] = a;
         if (out.top_k) {
-            if (tid < out.top_k && tid >= n_keys) first->all_top[part * out.top_k + tid] = 0;
-            for_top(sm.cand, n_keys, out.top_k, NT, [&](int r, u64 k) { first->all_top[part * out.top_k + r] = k; });
+            if (tid < out.top_k && tid >= n_keys) first->top[part * out.top_k + tid] = 0;
+            for_top(sm.cand, n_keys, out.top_k, NT, [&](int r, u64 k) { first->top[part * out.top_k + r] = k; });
         }
         cluster.sync();
         if (part != 0) return;
-        a = sm.all_sums[0];
-        for (int i = 1; i < parts; ++i) a.join(sm.all_sums[i], c);
-        keys = sm.all_top;
+        a = cs.sums[0];
+        for (int i = 1; i < parts; ++i) a.join(cs.sums[i], c);
+        keys = cs.top;
         n_keys = parts * out.top_k;
     }
     const float z_max = a.m * inv_tau;
@@ -602,11 +626,12 @@ template <typename T, int NT>
 void launch_forward(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float inv_tau, const int* targets,
                     const LogprobOut& out) {
     // few rows: as many blocks a row as give every SM two, while a thread still has a vector
-    int parts = 8;
+    int parts = NT > 32 ? 8 : 1;
     while (parts > 1 && ((long long)rows * parts > 2 * ctx.num_sms || V < parts * NT * RowVecs<T>::N)) parts /= 2;
     if (parts == 1) {
-        token_logprobs_kernel<T, NT, false><<<rows, NT, 0, ctx.stream>>>(logits, ld, V, inv_tau, targets, out, 1,
-                                                                         ctx.status);
+        constexpr int ROWS = BLOCK_OF<NT> / NT;
+        token_logprobs_kernel<T, NT, false><<<ceil_div(rows, ROWS), BLOCK_OF<NT>, 0, ctx.stream>>>(
+            logits, ld, rows, V, inv_tau, targets, out, 1, ctx.status);
         return;
     }
     cudaLaunchConfig_t cfg = {};
@@ -619,7 +644,7 @@ void launch_forward(const Ctx& ctx, const T* logits, long long ld, int rows, int
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, NT, true>, logits, ld, V, inv_tau, targets, out, parts, ctx.status);
+    cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, 128, true>, logits, ld, rows, V, inv_tau, targets, out, parts, ctx.status);
 }
 
 }  // namespace
@@ -627,7 +652,12 @@ void launch_forward(const Ctx& ctx, const T* logits, long long ld, int rows, int
 template <typename T>
 void launch_token_logprobs(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float temperature,
                            const int* targets, const LogprobOut& out) {
-    launch_forward<T, 128>(ctx, logits, ld, rows, V, 1.f / temperature, targets, out);
+    // A warp a row where the row is short, and with many rows up to 8192: no block to wait for (8192 rows of 1024 bf16
+    // logits 11.8 us against 22, of 8192 with five alternatives 40.7 against 50.8). Not for many alternatives: the
+    // bound of 32 threads' values is too loose for them.
+    const bool warp = out.top_k <= WALK && (V <= 2048 || (V <= 8192 && rows >= 8 * ctx.num_sms));
+    if (warp) launch_forward<T, 32>(ctx, logits, ld, rows, V, 1.f / temperature, targets, out);
+    else launch_forward<T, 128>(ctx, logits, ld, rows, V, 1.f / temperature, targets, out);
     ++*ctx.launches;
 }
 
