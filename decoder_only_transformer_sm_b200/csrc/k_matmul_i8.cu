@@ -8,7 +8,7 @@
 // Three kernels, chosen by the shape and the alignment of the operands:
 //   M <= 8, 16-byte rows   weight streaming (below): bound by reading B once
 //   M > 8, 16-byte rows    tcgen05 (kind::i8) with TMA operands
-//   other strides          dp4a on words put together from bytes
+//   other strides          tcgen05 with operands that warps put together from bytes
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -52,66 +52,6 @@ __device__ __forceinline__ f32x2 finish2(int a0, int a1, f32x2 sa, f32x2 sb, f32
         }
     }
     return u;
-}
-
-// ---------------------------------------------------------------- any strides
-// 64 x 64 outputs per block of 256 threads (4 x 4 each), 64 bytes of K staged at a
-// time as 32-bit words for dp4a. Rows may start at any byte: words are put together
-// from single bytes.
-constexpr int ST = 64, SKW = 16;
-
-template <int KIND, typename O>
-__global__ void __launch_bounds__(256) matmul_i8_simt_kernel(I8Product p) {
-    __shared__ int as[SKW][ST + 1], bs[SKW][ST + 1];
-    const int tiles_n = ceil_div(p.N, ST);
-    const int m0 = (int)(blockIdx.x / tiles_n) * ST, n0 = (int)(blockIdx.x % tiles_n) * ST;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    int acc[4][4] = {};
-    for (int k0 = 0; k0 < p.K; k0 += 4 * SKW) {
-        for (int i = threadIdx.x; i < SKW * ST; i += 256) {
-            const int r = i / SKW, w = i % SKW;
-            int a = 0, b = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = k0 + 4 * w + j;
-                if (k < p.K) {
-                    if (m0 + r < p.M) a |= (p.A[(long long)(m0 + r) * p.lda + k] & 0xff) << (8 * j);
-                    if (n0 + r < p.N) b |= (p.B[(long long)(n0 + r) * p.ldb + k] & 0xff) << (8 * j);
-                }
-            }
-            as[w][r] = a;
-            bs[w][r] = b;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < SKW; ++w) {
-            int a[4], b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = as[w][ty + 16 * i];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = bs[w][tx + 16 * j];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(a[i], b[j], acc[i][j]);
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = m0 + ty + 16 * i;
-        if (m >= p.M) continue;
-        const float sa = p.sa[m];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + tx + 16 * j;
-            if (n >= p.N) continue;
-            const float bias = KIND != EPI_STORE ? p.bias[n] : 0.f;
-            const float resid = KIND == EPI_BIAS_RESID ? p.resid[(long long)m * p.ldr + n] : 0.f;
-            reinterpret_cast<O*>(p.out)[(long long)m * p.ldo + n] =
-                finish<KIND, O>(acc[i][j], sa, p.sb[n], bias, resid);
-        }
-    }
 }
 
 // ---------------------------------------------------------------- few rows
@@ -216,16 +156,18 @@ void launch_rows(const Ctx& ctx, const I8Product& p) {
 // into one of two int32 accumulators in tensor memory; the epilogue warps read the other one (a lane
 // is a row), scale it and turn it around in shared memory, 32 rows of 128 bytes at a time, which leave
 // by a TMA store or as 16-byte stores of the warp (single elements where rows are not whole 16-byte segments). Rows and columns past the operands come as zeros from TMA and are not stored.
+// Rows that start anywhere (BYTES): eight more warps take the place of the TMA loads.
 // A pair shares its B rows, so a K block costs each CTA 32 KB of shared memory and of L2
 // traffic for 256 x 256 outputs a pair, where one CTA alone needs 48 KB for 128 x 256.
-template <int BN, int CTAS>
+template <int BN, int CTAS, bool BYTES = false>
 struct Tile {
     static constexpr int BM = 128, BK = 128;   // rows of a CTA
     static constexpr int B_ROWS = BN / CTAS;   // B rows in a CTA's shared memory
     static constexpr int A_BYTES = BM * BK, B_BYTES = B_ROWS * BK, STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = BN >= 128 ? 5 : 8;
     static constexpr int EPI_WARPS = BN >= 256 ? 16 : BN >= 128 ? 8 : 4;
-    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+    static constexpr int BYTE_WARPS = BYTES ? 8 : 0;
+    static constexpr int THREADS = 64 + 32 * (EPI_WARPS + BYTE_WARPS);
     static constexpr int WCOLS = BN / (EPI_WARPS / 4);   // columns of a warp
     static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int EPI_BUFS = BN >= 256 ? 1 : 2;   // a warp's staging buffers
@@ -325,12 +267,72 @@ __device__ __forceinline__ void put(uint8_t* at, const f32x2 (&v)[4], bf16) {
     *reinterpret_cast<uint4*>(at) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-template <int KIND, typename O, int BN, int CTAS>
-__global__ void __launch_bounds__(Tile<BN, CTAS>::THREADS, 1)
+// 16 bytes from k on of a row of K that starts at any byte, zeros past its end. lo .. hi: the
+// bytes of the whole operand; 32-bit words that touch others are put together from single bytes.
+__device__ __forceinline__ uint4 gather16(const int8_t* row, int k, int K, const int8_t* lo, const int8_t* hi) {
+    unsigned w[4] = {0, 0, 0, 0};
+    const int8_t* at = row + k;
+    const int off = (int)((uintptr_t)at & 3);
+    const unsigned* word = reinterpret_cast<const unsigned*>(at - off);
+    if (k + 16 <= K && at - off >= lo && at - off + 20 <= hi) {
+        unsigned u[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) u[i] = __ldg(word + i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(u[i], u[i + 1], 8 * off);
+    } else {
+        for (int i = 0; i < min(16, K - k); ++i) w[i >> 2] |= (unsigned)(uint8_t)at[i] << (8 * (i & 3));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One warp's part of a K block of 128 rows from row0 on, in the 128-byte-swizzle layout that TMA
+// writes: 16-byte pieces, four a lane. A block that is not the first along K and has 132 bytes left touches
+// no word outside the operand (rows past it are read as its last one, and not stored), so all its loads go
+// out before the first store; `edge` looks at each piece.
+struct Gather {
+    const int8_t* base;
+    long long ld;
+    int row0, rows;
+    static constexpr int PIECES = 128 * 8 / (8 * 32);   // 8 warps
+    __device__ __forceinline__ void load(unsigned (&u)[PIECES][5], int (&off)[PIECES], int k0, int i0) const {
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            const int i = i0 + 256 * j;
+            const int8_t* at = base + (long long)min(row0 + (i >> 3), rows - 1) * ld + k0 + 16 * (i & 7);
+            off[j] = (int)((uintptr_t)at & 3);
+            const unsigned* word = reinterpret_cast<const unsigned*>(at - off[j]);
+#pragma unroll
+            for (int w = 0; w < 5; ++w) u[j][w] = __ldg(word + w);
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t* dst, const unsigned (&u)[PIECES][5], const int (&off)[PIECES], int i0) const {
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            const int i = i0 + 256 * j, sh = 8 * off[j];
+            *reinterpret_cast<uint4*>(dst + seg(i >> 3, i & 7)) =
+                make_uint4(__funnelshift_r(u[j][0], u[j][1], sh), __funnelshift_r(u[j][1], u[j][2], sh),
+                           __funnelshift_r(u[j][2], u[j][3], sh), __funnelshift_r(u[j][3], u[j][4], sh));
+        }
+    }
+    __device__ __forceinline__ void edge(uint8_t* dst, int k0, int K, int i0) const {
+        const int8_t* hi = base + (long long)(rows - 1) * ld + K;
+#pragma unroll 1
+        for (int j = 0; j < PIECES; ++j) {
+            const int i = i0 + 256 * j, r = row0 + (i >> 3), k = k0 + 16 * (i & 7);
+            *reinterpret_cast<uint4*>(dst + seg(i >> 3, i & 7)) =
+                r < rows && k < K ? gather16(base + (long long)r * ld, k, K, base, hi) : make_uint4(0, 0, 0, 0);
+        }
+    }
+};
+
+template <int KIND, typename O, int BN, int CTAS, bool BYTES = false>
+__global__ void __launch_bounds__(Tile<BN, CTAS, BYTES>::THREADS, 1)
     matmul_i8_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmO, I8Product p, TileGrid grid, unsigned* status) {
-    using L = Tile<BN, CTAS>;
+    using L = Tile<BN, CTAS, BYTES>;
     constexpr bool PAIR = CTAS == 2;
+    static_assert(!BYTES || (BN == 128 && CTAS == 1), "rows that start anywhere: 128 x 128 tiles");
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* epi = smem + L::STAGES * L::STAGE_BYTES;
     TileCtl* ctl = reinterpret_cast<TileCtl*>(epi + L::EPI_WARPS * L::EPI_BUFS * EPI_ROWS + L::EPI_COLS);
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(Tile<BN, CTAS>::THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::STAGES; ++s) {
-            tc::mbar_init(&ctl->full[s], 1);
+            tc::mbar_init(&ctl->full[s], BYTES ? L::BYTE_WARPS : 1);
             tc::mbar_init(&ctl->empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -369,8 +371,38 @@ __global__ void __launch_bounds__(Tile<BN, CTAS>::THREADS, 1)
     tc::fence_after_sync();
     const uint32_t tmem = ctl->tmem_base;
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (BYTES && warp >= 2 + L::EPI_WARPS) {
+        const int bw = warp - 2 - L::EPI_WARPS;
+        uint32_t it = 0, ok = 1;
+        for (int u = first; u < tiles && ok; u += step) {
+            int mb, nb;
+            grid.at(u, mb, nb);
+            for (int kb = 0; kb < grid.k_blocks; ++kb, ++it) {
+                const int s = it % L::STAGES;
+                if (lane == 0) ok = tc::mbar_wait(&ctl->empty[s], ((it / L::STAGES) & 1) ^ 1, abort, status) ? 1u : 0u;
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                uint8_t* sa = smem + s * L::STAGE_BYTES;
+                const Gather ga = {p.A, p.lda, mb * L::BM, p.M}, gb = {p.B, p.ldb, nb * BN, p.N};
+                const int k0 = kb * L::BK, i0 = bw * 32 + lane;
+                if (kb > 0 && k0 + 132 <= p.K) {
+                    unsigned ua[Gather::PIECES][5], ub[Gather::PIECES][5];
+                    int oa[Gather::PIECES], ob[Gather::PIECES];
+                    ga.load(ua, oa, k0, i0);
+                    gb.load(ub, ob, k0, i0);
+                    ga.store(sa, ua, oa, i0);
+                    gb.store(sa + L::A_BYTES, ub, ob, i0);
+                } else {
+                    ga.edge(sa, k0, p.K, i0);
+                    gb.edge(sa + L::A_BYTES, k0, p.K, i0);
+                }
+                tc::fence_proxy_async_smem();   // the MMA reads through the async proxy
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&ctl->full[s]);
+            }
+        }
+    } else if (warp == 0) {
+        if (lane == 0 && !BYTES) {
             tc::tma_prefetch_desc(&tmA);
             tc::tma_prefetch_desc(&tmB);
             uint32_t it = 0;
@@ -616,11 +648,11 @@ void allow_smem(F* kernel, size_t bytes, std::atomic<unsigned long long>& done) 
 
 bool whole_segments(const void* p, long long ld, int es) { return ((uintptr_t)p & 15) == 0 && (ld * es) % 16 == 0; }
 
-template <int KIND, typename O, int BN, int CTAS>
+template <int KIND, typename O, int BN, int CTAS, bool BYTES = false>
 bool launch_tc(const Ctx& ctx, const I8Product& p) {
-    using L = Tile<BN, CTAS>;
+    using L = Tile<BN, CTAS, BYTES>;
     constexpr int CW = 128 / (int)sizeof(O);
-    CUtensorMap ta, tb, to;
+    CUtensorMap ta = {}, tb = {}, to = {};   // zeros where not used
     const CUtensorMapDataType I8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     TileGrid g;
     g.tiles_m = ceil_div(p.M, L::BM * CTAS);
@@ -630,20 +662,19 @@ bool launch_tc(const Ctx& ctx, const I8Product& p) {
     g.m_fastest = p.M < p.N;
     g.vec_out = whole_segments(p.out, p.ldo, sizeof(O));
     g.vec_resid = KIND == EPI_BIAS_RESID && whole_segments(p.resid, p.ldr, 4);
-    if (!make_map(&ta, I8, 1, p.A, p.M, p.K, p.lda, L::BK, L::BM) ||
-        !make_map(&tb, I8, 1, p.B, p.N, p.K, p.ldb, L::BK, L::B_ROWS))
+    if (!BYTES && (!make_map(&ta, I8, 1, p.A, p.M, p.K, p.lda, L::BK, L::BM) ||
+        !make_map(&tb, I8, 1, p.B, p.N, p.K, p.ldb, L::BK, L::B_ROWS)))
         return false;
     // TMA stores are asynchronous, but their bursts hold up the operands' loads: they pay for fp32 results
     // and short sums (16384 x 2304 in bf16: K = 128 21 us against 27 with plain stores, K = 768 35.6 against 33.4).
-    g.tma_out = g.vec_out && (sizeof(O) == 4 || g.k_blocks <= 4);
+    // They write whole 16-byte segments, so a row that ends inside one (its padding is the caller's) is not theirs.
+    g.tma_out = g.vec_out && (p.N * sizeof(O)) % 16 == 0 && (sizeof(O) == 4 || g.k_blocks <= 4);
     if (g.tma_out) {
         if (!make_map(&to, sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                       sizeof(O), p.out, p.M, p.N, p.ldo, CW, 32))
             return false;
-    } else {
-        to = ta;   // not used
     }
-    auto kernel = matmul_i8_tc_kernel<KIND, O, BN, CTAS>;
+    auto kernel = matmul_i8_tc_kernel<KIND, O, BN, CTAS, BYTES>;
     static std::atomic<unsigned long long> done{0};
     allow_smem(kernel, tile_smem<L>(), done);
     cudaLaunchConfig_t cfg = {};
@@ -687,9 +718,7 @@ bool launch_kind(const Ctx& ctx, const I8Product& p) {
         if (t256 <= t128 && t256 <= t64) return launch_tc<KIND, O, 256, 2>(ctx, p);
         return t128 <= t64 ? launch_tc<KIND, O, 128, 1>(ctx, p) : launch_tc<KIND, O, 64, 1>(ctx, p);
     }
-    const long long tiles = (long long)ceil_div(p.N, ST) * ceil_div(p.M, ST);
-    matmul_i8_simt_kernel<KIND, O><<<(unsigned)tiles, 256, 0, ctx.stream>>>(p);
-    return true;
+    return launch_tc<KIND, O, 128, 1, true>(ctx, p);
 }
 
 }  // namespace

@@ -151,12 +151,15 @@ def test_products(M, N, K, epilogue, out_dtype):
     _product(M, N, K, epilogue, out_dtype, pads=(-K % 16, -K % 16, 0, 0))
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 40, 33), (3, 40, 768), (40, 70, 65), (130, 129, 257)])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 33), (3, 41, 768), (40, 70, 65), (130, 129, 257), (700, 2401, 99)])
 @pytest.mark.parametrize("pads,shift", [((0, 0, 0, 0), (0, 0, 0)), ((1, 7, 3, 5), (0, 0, 0)),
                                         ((16, 32, 1, 2), (16, 32, 1)), ((0, 0, 8, 8), (3, 1, 8)),
-                                        ((15, 0, 7, 1), (1, 0, 3))])
+                                        ((15, 0, 7, 1), (1, 0, 3)), ("whole", (16, 32, 0))])
 def test_strides_and_starts(M, N, K, pads, shift):
-    for epilogue, dtype in (("store", torch.bfloat16), ("bias_gelu", torch.bfloat16), ("bias_resid", torch.float32)):
+    if pads == "whole":   # operands' rows of whole 16 bytes, the results' ending inside one; what pads them is not zero
+        pads = (-K % 16, 16 + -K % 16, -N % 8, -N % 4)
+    for epilogue, dtype in (("store", torch.bfloat16), ("bias_gelu", torch.bfloat16), ("bias_resid", torch.float32),
+                            ("bias", torch.float32)):
         _product(M, N, K, epilogue, dtype, pads=pads, shift=shift)
 
 
