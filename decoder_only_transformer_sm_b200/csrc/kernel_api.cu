@@ -211,6 +211,7 @@ extern "C" int gpt2k_embedding_bwd(const int32_t* idx, const float* dx, int B, i
 namespace {
 bool misaligned(const void* p, size_t bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
 size_t elem_size(int dtype) { return dtype == GPT2K_F32 ? 4 : 2; }
+constexpr int MAX_EXTENT = 1 << 30;   // rows, columns: 32-bit index arithmetic has room past them
 }  // namespace
 
 extern "C" int gpt2k_quantize_rows(int dtype, const void* x, int rows, int K, int64_t ldx, int8_t* q, int64_t ldq,
@@ -218,6 +219,7 @@ extern "C" int gpt2k_quantize_rows(int dtype, const void* x, int rows, int K, in
     if (dtype != GPT2K_F32 && dtype != GPT2K_BF16) return set_error(GPT2_ERR_INVALID_ARG, "unknown dtype");
     if (rows < 1 || K < 1 || ldx < K || ldq < K)
         return set_error(GPT2_ERR_INVALID_ARG, "need rows, K >= 1 and row strides >= K");
+    if (rows > MAX_EXTENT || K > MAX_EXTENT) return set_error(GPT2_ERR_INVALID_ARG, "rows or K above 2^30");
     if (!x || !q || !scale) return set_error(GPT2_ERR_INVALID_ARG, "NULL operand");
     if (misaligned(x, elem_size(dtype)) || misaligned(scale, 4))
         return set_error(GPT2_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
@@ -241,6 +243,7 @@ extern "C" int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scal
     if (out_dtype != GPT2K_F32 && out_dtype != GPT2K_BF16) return set_error(GPT2_ERR_INVALID_ARG, "unknown dtype");
     if (M < 1 || N < 1 || K < 1 || lda < K || ldb < K || ldo < N)
         return set_error(GPT2_ERR_INVALID_ARG, "need M, N, K >= 1, lda, ldb >= K and ldo >= N");
+    if (M > MAX_EXTENT || N > MAX_EXTENT) return set_error(GPT2_ERR_INVALID_ARG, "M or N above 2^30");
     if (K > I8_MAX_K) return set_error(GPT2_ERR_INVALID_ARG, "K above 131071: a 32-bit sum could overflow");
     if (!A || !a_scale || !B || !b_scale || !out || !status_dev) return set_error(GPT2_ERR_INVALID_ARG, "NULL operand");
     if (epilogue != GPT2K_EPI_STORE && !bias) return set_error(GPT2_ERR_INVALID_ARG, "epilogue operand missing");
@@ -289,8 +292,8 @@ int check_logprob_args(int dtype, const void* logits, int rows, int V, int64_t l
     if (!logits || !status) return set_error(GPT2_ERR_INVALID_ARG, "NULL operand");
     if (!(temperature > 0.f) || !(temperature < INFINITY) || !(1.5f / temperature < INFINITY))
         return set_error(GPT2_ERR_INVALID_ARG, "temperature must be finite and > 0, 1.5 / temperature finite");
-    if ((long long)rows * (V / 2048 + 1) > 0x7fffffffll)
-        return set_error(GPT2_ERR_INVALID_ARG, "rows x V is more than one launch takes");
+    if (V > MAX_EXTENT || (long long)rows * (V / 2048 + 1) > MAX_EXTENT)
+        return set_error(GPT2_ERR_INVALID_ARG, "V above 2^30, or rows x V more than one launch takes");
     if (misaligned(logits, elem_size(dtype)) || misaligned(status, 4))
         return set_error(GPT2_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
     return GPT2_OK;

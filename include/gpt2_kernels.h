@@ -174,7 +174,9 @@ int gpt2k_embedding_bwd_workspace(int B, int T, int C, int64_t* floats);
 /* ---- 8-bit linear layers --------------------------------------------------
  * nn.Linear on a trained model's weights with 8-bit operands: weights (N, K)
  * quantised once by output channel, activations (M, K) by token before each
- * product, both with gpt2k_quantize_rows. */
+ * product, both with gpt2k_quantize_rows. These calls and the log-probabilities'
+ * below run on the current device, which must be the buffers' and the stream's;
+ * they allocate nothing, hold no state and may be captured into graphs. */
 
 /* Symmetric quantisation of each row of x (rows, K) in dtype, row stride ldx
  * elements: with a = max_k |x[r][k]|,
@@ -185,8 +187,8 @@ int gpt2k_embedding_bwd_workspace(int B, int T, int C, int64_t* floats);
  * left as they are. A row of zeros has scale 0 and codes 0; a row with a NaN or
  * an infinity has scale NaN and codes 0, so that its products are NaN. x and q
  * may start anywhere an element may; 16-byte aligned rows are fastest. Errors:
- * INVALID_ARG (unknown dtype, rows or K < 1, a stride below K, a NULL or
- * misaligned pointer). */
+ * INVALID_ARG (unknown dtype, rows or K < 1 or above 2^30, a stride below K, a
+ * NULL or misaligned pointer). */
 int gpt2k_quantize_rows(int dtype, const void* x, int rows, int K, int64_t ldx, int8_t* q, int64_t ldq,
                         float* scale, void* stream);
 
@@ -202,10 +204,10 @@ int gpt2k_quantize_rows(int dtype, const void* x, int rows, int K, int64_t ldx, 
  *                        resid fp32, row stride ldr; it may be out itself)
  * out has row stride ldo elements; columns N .. ldo - 1 are left as they are.
  * out must not overlap A or B. Operands may start anywhere an element may:
- * A and B whose first byte and row stride are multiples of 16 take the tensor
- * cores or, for a few rows, the weight-streaming kernel; other ones a slower
- * kernel. Errors: INVALID_ARG (sizes < 1, K > 131071, a stride below its row,
- * another epilogue, an operand of the epilogue missing, bias_resid with a bf16
+ * A and B whose first byte and row stride are multiples of 16 are loaded by
+ * TMA or, for a few rows, streamed; other ones are put together from bytes
+ * (slower). Errors: INVALID_ARG (sizes < 1, M or N above 2^30, K > 131071, a
+ * stride below its row, another epilogue, an operand of the epilogue missing, bias_resid with a bf16
  * result, a NULL or misaligned pointer). */
 int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B, int64_t ldb,
                     const float* b_scale, int M, int N, int K, int epilogue, int out_dtype, void* out, int64_t ldo,
@@ -229,7 +231,7 @@ int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scale, const in
  * lse, entropy, top_logp and a given target's logp; its ids are ordered with
  * NaN above every number. A target outside [-1, V) sets status bit 0 and is
  * clamped into [0, V). Errors: INVALID_ARG (unknown dtype, rows or V < 1,
- * ld < V, a temperature that is not finite and > 0 or below 4.5e-39 (1.5 /
+ * V > 2^30 or rows * (V / 2048 + 1) > 2^30, ld < V, a temperature that is not finite and > 0 or below 4.5e-39 (1.5 /
  * temperature infinite), arguments that do not go together, a NULL or misaligned pointer). */
 int gpt2k_token_logprobs(int dtype, const void* logits, int rows, int V, int64_t ld, float temperature,
                          const int32_t* targets, int top_k, float* logp, float* entropy, float* lse,

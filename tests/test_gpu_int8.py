@@ -170,6 +170,31 @@ def test_largest_sums(M, pad):
     _product(M, 24, 131071, "store", torch.float32, pads=(pad, pad, 0, 0), extreme=True)
 
 
+@pytest.mark.parametrize("M", [3, 20])
+@pytest.mark.parametrize("odd", [0, 1])
+def test_rows_far_apart(M, odd):
+    """Offsets past 32 bits: rows of A, of the codes written and of the results lie over 2^31 bytes in all apart."""
+    from decoder_only_transformer_sm_b200 import native
+    K, N = 256, 40
+    ld = (1 << 32) // M // 16 * 16 + 16 + odd
+    hold = torch.empty((M - 1) * ld + K, dtype=torch.int8, device="cuda")
+    q = hold.as_strided((M, K), (ld, 1))
+    g = torch.Generator().manual_seed(M)
+    x = torch.randn((M, K), generator=g)
+    s = torch.empty(M, device="cuda")
+    native.quantize_rows(x.cuda(), q, s)
+    want_q, want_s = _codes64(x.numpy())
+    assert torch.equal(q.cpu(), torch.from_numpy(want_q)) and torch.equal(s.cpu(), torch.from_numpy(want_s))
+    b = torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int8).cuda()
+    sb = torch.rand(N, generator=g).cuda()
+    ldo = (1 << 31) // M // 4 * 4 + 4 + odd
+    room = torch.empty((M - 1) * ldo + N, dtype=torch.bfloat16, device="cuda")
+    out = room.as_strided((M, N), (ldo, 1))
+    native.matmul_i8(q, s, b, sb, out)
+    want = (q.double() @ b.double().t()) * s.double()[:, None] * sb.double()
+    assert torch.all((out.double() - want).abs() <= (2.0 ** -8 * 1.01 + 4 * 2.0 ** -24) * want.abs())
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 64, 64), (150, 264, 320)])
 def test_residual_in_place(M, N, K):
     _product(M, N, K, "bias_resid", torch.float32, in_place=True)

@@ -12,7 +12,9 @@ log p = d - log s and lse = m + log s add a rounding of the result and the error
 and the entropy log s - w / s the same error again, weighted by |d| <= 40 in the worst
 term: sum p |d| (2^-21 + ...) <= (H + 2) of it. Gradients: p = e^(z - lse) has the relative
 error 6 eps (|z| + |lse|) + 2^-21, its factor g + h (log p + H) the absolute one
-|h| (6 eps (|z| + |lse| + H)) + 3 eps of its parts; a bf16 result adds 2^-8."""
+|h| (6 eps (|z| + |lse| + H)) + 3 eps of its parts; a bf16 result adds 2^-8. A p below the
+smallest normal number, 2^-126, is flushed to zero (ex2.approx.ftz): it is off by less than 2^-126, and its product with
+its factor by less than 2^-126 of that (with a factor of 100 that is 1.2e-36)."""
 import numpy as np
 import pytest
 
@@ -211,7 +213,7 @@ def test_bad_targets_are_reported():
     assert int(status.item()) == 1
 
 
-def _check_backward(x, tau, pad=0, shift=0, seed=0, use=("logp", "entropy"), in_place=False):
+def _check_backward(x, tau, pad=0, shift=0, seed=0, use=("logp", "entropy"), in_place=False, dpad=None, dshift=None):
     from decoder_only_transformer_sm_b200 import native
     R, V = x.shape
     rng = np.random.default_rng(seed)
@@ -225,6 +227,7 @@ def _check_backward(x, tau, pad=0, shift=0, seed=0, use=("logp", "entropy"), in_
     if in_place:
         dhold, dd = hold, dx
     else:
+        pad, shift = pad if dpad is None else dpad, shift if dshift is None else dshift   # of dlogits from here on
         dhold, dd = _place(torch.full_like(x, 7.0), pad, shift)
     cu = lambda v: None if v is None else torch.from_numpy(v).cuda()  # noqa: E731
     status = native.token_logprobs_bwd(dx, V, tau, cu(lse), dd, targets=cu(targets) if g is not None else None,
@@ -244,6 +247,7 @@ def _check_backward(x, tau, pad=0, shift=0, seed=0, use=("logp", "entropy"), in_
         size = np.minimum(size, 2 * np.where(np.isfinite(L), np.abs(L), 0.0) + 110.0)
         tol = np.where(p == 0, 0.0, np.abs(want) * (6 * EPS * 2 * size + 2.0 ** -21 + 4 * EPS) + p *
                        (np.abs(hh) * 6 * EPS * (2 * size + np.abs(Hd)) + 3 * EPS * (np.abs(gg) + np.abs(hh) * (size + np.abs(Hd)))))
+        tol = tol + np.where(p == 0, 0.0, 2.0 ** -126 * np.abs(inner))   # p flushed to zero
     one = np.zeros_like(want)
     one[np.arange(R), np.maximum(targets, 0)] = 1.0
     want = np.where(L == -np.inf, 0.0, want + one * gg)
@@ -274,6 +278,37 @@ def test_gradient_strides_starts_and_in_place(dtype, pad, shift, in_place):
     for R, V in ((1, 333), (40, 5003), (400, 64)):
         kinds = [KINDS[i % len(KINDS)] for i in range(R)]
         _check_backward(_rows(kinds, V, dtype, pad), 1.3, pad=pad, shift=shift, seed=shift, in_place=in_place)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("pad,shift,dpad,dshift", [(0, 0, 1, 0), (3, 0, 0, 1), (8, 2, 8, 3), (1, 1, 5, 0)])
+def test_gradient_laid_out_apart_from_the_logits(dtype, pad, shift, dpad, dshift):
+    for R, V in ((2, 50), (30, 5003)):
+        kinds = [KINDS[i % len(KINDS)] for i in range(R)]
+        _check_backward(_rows(kinds, V, dtype, pad), 0.8, pad=pad, shift=shift, dpad=dpad, dshift=dshift)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_far_apart(dtype):
+    """Offsets past 32 bits: three rows 2^30 + 8 elements apart, forward and gradient."""
+    from decoder_only_transformer_sm_b200 import native
+    V, ld = 5000, (1 << 30) + 8
+    hold = torch.empty(2 * ld + V, dtype=dtype, device="cuda")
+    x = hold.as_strided((3, V), (ld, 1))
+    x.copy_(torch.randn((3, V), generator=torch.Generator().manual_seed(1)).to(dtype))
+    t = torch.tensor([1, 4999, 77], dtype=torch.int32, device="cuda")
+    logp, lse = torch.empty(3, device="cuda"), torch.empty(3, device="cuda")
+    ids, top = torch.empty((3, 2), dtype=torch.int32, device="cuda"), torch.empty((3, 2), device="cuda")
+    native.token_logprobs(x, V, 1.0, targets=t, logp=logp, lse=lse, top_ids=ids, top_logp=top)
+    near = x.clone()
+    want = torch.log_softmax(near.double(), 1)
+    assert torch.all((logp.double() - want.gather(1, t.long()[:, None])[:, 0]).abs() < 2e-5)
+    assert torch.equal(ids.long(), torch.sort(near.float(), dim=1, descending=True, stable=True).indices[:, :2])
+    g = torch.tensor([1.0, -2.0, 0.5], device="cuda")
+    native.token_logprobs_bwd(x, V, 1.0, lse, x, targets=t, dlogp=g)
+    grad = -g.double()[:, None] * want.exp()
+    grad[torch.arange(3), t.long()] += g.double()
+    assert torch.all((x.double() - grad).abs() <= 2.0 ** -8 * 1.01 * grad.abs() + 1e-6)
 
 
 def test_gradient_against_differences():

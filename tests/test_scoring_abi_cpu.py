@@ -24,7 +24,8 @@ def test_quantize_rows_refusals():
     lib = native.load_library()
     ok = (1, P, 4, 8, 8, P, 8, P, None)
     _refused(lib.gpt2k_quantize_rows, ok,
-             [{0: 2}, {2: 0}, {3: 0}, {4: 7}, {6: 7}, {1: None}, {5: None}, {7: None}, {1: ODD}, {7: ODD}])
+             [{0: 2}, {2: 0}, {3: 0}, {4: 7}, {6: 7}, {1: None}, {5: None}, {7: None}, {1: ODD}, {7: ODD}, {2: (1 << 30) + 1},
+              {3: (1 << 30) + 1, 4: 1 << 31, 6: 1 << 31}])
 
 
 def test_matmul_i8_refusals():
@@ -34,6 +35,7 @@ def test_matmul_i8_refusals():
     _refused(lib.gpt2k_matmul_i8, ok,
              [{6: 0}, {7: 0}, {8: 0}, {1: 15}, {4: 15}, {12: 7}, {9: 4}, {9: 5}, {9: -1}, {10: 2},
               {1: 1 << 20, 4: 1 << 20, 8: 131072},                     # sums could pass 32 bits
+              {6: (1 << 30) + 1}, {7: (1 << 30) + 1, 12: 1 << 31, 15: 1 << 31},
               {0: None}, {2: None}, {3: None}, {5: None}, {11: None}, {16: None},
               {13: None},                                              # bias wanted
               {9: 3},                                                  # bias_resid writes fp32
@@ -47,6 +49,7 @@ def test_token_logprobs_refusals():
     ok = (1, P, 3, 40, 40, 1.0, P, 5, P, P, P, P, P, P, None)
     _refused(lib.gpt2k_token_logprobs, ok,
              [{0: 2}, {2: 0}, {3: 0}, {4: 39}, {5: 0.0}, {5: -1.0}, {5: float("nan")}, {5: float("inf")}, {5: 1e-39},
+              {2: (1 << 30) + 1}, {2: 1 << 20, 3: 1 << 22, 4: 1 << 22},
               {1: None}, {13: None}, {6: None}, {8: None}, {7: 33}, {7: -1}, {3: 4, 4: 4}, {11: None}, {12: None},
               {7: 0}, {6: None, 8: None, 9: None, 10: None, 7: 0, 11: None, 12: None}, {1: ODD}, {10: ODD}])
 
