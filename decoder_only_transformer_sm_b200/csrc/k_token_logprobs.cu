@@ -417,29 +417,20 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
     Sums a = {LOWEST, 0.f, 0.f};
     float largest = NEG_INF;
     {
-        // batches of U whole vectors, the next one's loads under way
+        // batches of U whole vectors
         int i = begin + tid;
         const uint4* at = reinterpret_cast<const uint4*>(x + rv.head);
         const int stop = min(end, rv.full) - (U - 1) * NT;
         uint4 q[U];
-        if (i < stop) {
+        for (; i < stop; i += U * NT) {
 #pragma unroll
             for (int u = 0; u < U; ++u) q[u] = __ldg(at + i + u * NT);
-        }
-        for (; i < stop; i += U * NT) {
-            uint4 next[U];
-            if (i + U * NT < stop) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) next[u] = __ldg(at + i + (U + u) * NT);
-            }
             float top, low;
             extremes(q, top, low, T());
             largest = fmaxf(largest, top);
             if (top > a.m) a.raise(top, c);
             if (low > -1e30f) a.add<false, T>(q, c);
             else a.add<true, T>(q, c);
-#pragma unroll
-            for (int u = 0; u < U; ++u) q[u] = next[u];
         }
         // what is left: fewer than U vectors, and the row's ends
         if (i < end) {
@@ -622,21 +613,21 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, lo
     }
 }
 
+// NT threads a row.
 template <typename T, int NT>
-void launch_forward(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float inv_tau, const int* targets,
-                    const LogprobOut& out) {
-    // few rows: as many blocks a row as give every SM two, while a thread still has a vector
-    int parts = NT > 32 ? 8 : 1;
-    while (parts > 1 && ((long long)rows * parts > 2 * ctx.num_sms || V < parts * NT * RowVecs<T>::N)) parts /= 2;
-    if (parts == 1) {
-        constexpr int ROWS = BLOCK_OF<NT> / NT;
-        token_logprobs_kernel<T, NT, false><<<ceil_div(rows, ROWS), BLOCK_OF<NT>, 0, ctx.stream>>>(
-            logits, ld, rows, V, inv_tau, targets, out, 1, ctx.status);
-        return;
-    }
+void launch_rows(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float inv_tau, const int* targets,
+                 const LogprobOut& out) {
+    token_logprobs_kernel<T, NT, false><<<ceil_div(rows, BLOCK_OF<NT> / NT), BLOCK_OF<NT>, 0, ctx.stream>>>(
+        logits, ld, rows, V, inv_tau, targets, out, 1, ctx.status);
+}
+
+// A cluster of `parts` blocks of 128 threads a row.
+template <typename T>
+void launch_split(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float inv_tau, const int* targets,
+                  const LogprobOut& out, int parts) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(rows * parts);
-    cfg.blockDim = dim3(NT);
+    cfg.blockDim = dim3(128);
     cfg.stream = ctx.stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -644,7 +635,8 @@ void launch_forward(const Ctx& ctx, const T* logits, long long ld, int rows, int
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, 128, true>, logits, ld, rows, V, inv_tau, targets, out, parts, ctx.status);
+    cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, 128, true>, logits, ld, rows, V, inv_tau, targets, out, parts,
+                       ctx.status);
 }
 
 }  // namespace
@@ -652,12 +644,21 @@ void launch_forward(const Ctx& ctx, const T* logits, long long ld, int rows, int
 template <typename T>
 void launch_token_logprobs(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float temperature,
                            const int* targets, const LogprobOut& out) {
+    const float inv_tau = 1.f / temperature;
     // A warp a row where the row is short, and with many rows up to 8192: no block to wait for (8192 rows of 1024 bf16
     // logits 11.8 us against 22, of 8192 with five alternatives 40.7 against 50.8). Not for many alternatives: the
     // bound of 32 threads' values is too loose for them.
     const bool warp = out.top_k <= WALK && (V <= 2048 || (V <= 8192 && rows >= 8 * ctx.num_sms));
-    if (warp) launch_forward<T, 32>(ctx, logits, ld, rows, V, 1.f / temperature, targets, out);
-    else launch_forward<T, 128>(ctx, logits, ld, rows, V, 1.f / temperature, targets, out);
+    // Few rows: as many blocks a row as give every SM two, while a thread still has a vector.
+    int parts = 8;
+    while (parts > 1 && ((long long)rows * parts > 2 * ctx.num_sms || V < parts * 128 * RowVecs<T>::N)) parts /= 2;
+    // 256 threads for rows of 120 KB and more: with 128, the rows under way together are more than L2 holds, and what
+    // is read again comes from memory (4096 x 131072 bf16, five alternatives: 193 us against 254; 8192 x 16384: 79
+    // against 60).
+    if (warp) launch_rows<T, 32>(ctx, logits, ld, rows, V, inv_tau, targets, out);
+    else if (parts > 1) launch_split<T>(ctx, logits, ld, rows, V, inv_tau, targets, out, parts);
+    else if (V >= 120000 / (int)sizeof(T)) launch_rows<T, 256>(ctx, logits, ld, rows, V, inv_tau, targets, out);
+    else launch_rows<T, 128>(ctx, logits, ld, rows, V, inv_tau, targets, out);
     ++*ctx.launches;
 }
 

@@ -157,21 +157,21 @@ def _check_forward(x, tau, k, pad=0, shift=0, seed=0, only=("logp", "entropy", "
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("V", [1, 2, 31, 32, 33, 100, 255, 1021, 1024, 2048, 4097, 8191, 16384, 50257])
-@pytest.mark.parametrize("k", [0, 1, 5, 32])
+@pytest.mark.parametrize("V", [1, 2, 31, 32, 33, 100, 255, 1021, 1024, 2048, 4097, 8191, 16384, 50257, 70001])
+@pytest.mark.parametrize("k", [0, 1, 5, 9, 32])
 def test_every_kind_of_row(dtype, V, k):
     x = _rows(KINDS * 2, V, dtype, V + k)
     _check_forward(x, 1.0, min(k, V), pad=-V % 8, seed=V)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("R", [1, 2, 5, 9, 40, 75, 149, 300, 700])
-@pytest.mark.parametrize("V", [700, 50257])
+@pytest.mark.parametrize("R", [1, 2, 5, 9, 40, 75, 149, 300, 700, 1300])
+@pytest.mark.parametrize("V", [700, 5003, 50257, 70001])
 def test_row_counts(dtype, R, V):
-    """Few rows are split over more blocks than many."""
+    """Few rows are split over more blocks than many; many short ones take a warp each."""
     kinds = [KINDS[(i * 5) % len(KINDS)] for i in range(R)]
-    if R > 100 and V > 1000:
-        kinds = kinds[:150]
+    if V > 6000:
+        kinds = kinds[:330 if V > 60000 and R == 1300 else 150]
     _check_forward(_rows(kinds, V, dtype, R), 0.8, 5, pad=-V % 8, seed=R)
 
 
