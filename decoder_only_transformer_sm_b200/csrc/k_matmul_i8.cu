@@ -75,6 +75,8 @@ template <int KIND, typename O, int MM, int RG>
 __global__ void __launch_bounds__(GV_THREADS) matmul_i8_rows_kernel(I8Product p) {
     const int lane = threadIdx.x & 31;
     const int n0 = (blockIdx.x * (GV_THREADS / 32) + (threadIdx.x >> 5)) * RG;
+    griddep_wait();     // nothing is read or written before the kernel before this one has ended
+    griddep_launch();   // and the next one's blocks may come as soon as all of this one's have
     if (n0 >= p.N) return;
     const int chunks = p.K / 16;
     const int4* b[RG];
@@ -144,9 +146,9 @@ void launch_rows(const Ctx& ctx, const I8Product& p) {
     // four rows a warp once that leaves every SM eight warps, else one
     constexpr int W = GV_THREADS / 32;
     if (p.N >= 4 * 8 * ctx.num_sms)
-        matmul_i8_rows_kernel<KIND, O, MM, 4><<<ceil_div(p.N, 4 * W), GV_THREADS, 0, ctx.stream>>>(p);
+        launch_pdl(ctx, matmul_i8_rows_kernel<KIND, O, MM, 4>, dim3(ceil_div(p.N, 4 * W)), dim3(GV_THREADS), 0, p);
     else
-        matmul_i8_rows_kernel<KIND, O, MM, 1><<<ceil_div(p.N, W), GV_THREADS, 0, ctx.stream>>>(p);
+        launch_pdl(ctx, matmul_i8_rows_kernel<KIND, O, MM, 1>, dim3(ceil_div(p.N, W)), dim3(GV_THREADS), 0, p);
 }
 
 // ---------------------------------------------------------------- tensor cores
@@ -355,6 +357,7 @@ __global__ void __launch_bounds__(Tile<BN, CTAS, BYTES>::THREADS, 1)
         ctl->abort = 0;
         tc::fence_barrier_init();
     }
+    griddep_wait();   // also before the allocation: tensor memory is not held while the kernel before may want it
     if (warp == 1) {
         if (PAIR) {
             tc::tmem_alloc_pair(&ctl->tmem_base, L::TMEM_COLS);
@@ -370,6 +373,7 @@ __global__ void __launch_bounds__(Tile<BN, CTAS, BYTES>::THREADS, 1)
     else __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = ctl->tmem_base;
+    griddep_launch();
 
     if (BYTES && warp >= 2 + L::EPI_WARPS) {
         const int bw = warp - 2 - L::EPI_WARPS;
@@ -677,18 +681,8 @@ bool launch_tc(const Ctx& ctx, const I8Product& p) {
     auto kernel = matmul_i8_tc_kernel<KIND, O, BN, CTAS, BYTES>;
     static std::atomic<unsigned long long> done{0};
     allow_smem(kernel, tile_smem<L>(), done);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(CTAS * min(g.tiles_m * g.tiles_n, ctx.num_sms / CTAS));
-    cfg.blockDim = dim3(L::THREADS);
-    cfg.dynamicSmemBytes = tile_smem<L>();
-    cfg.stream = ctx.stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CTAS;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = CTAS > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, ta, tb, to, p, g, ctx.status) == cudaSuccess;
+    return launch_pdl_clusters(ctx, CTAS, kernel, dim3(CTAS * min(g.tiles_m * g.tiles_n, ctx.num_sms / CTAS)),
+                               dim3(L::THREADS), tile_smem<L>(), ta, tb, to, p, g, ctx.status) == cudaSuccess;
 }
 
 template <int KIND, typename O>

@@ -75,6 +75,8 @@ __global__ void __launch_bounds__(256) quantize_long_rows_kernel(const T* __rest
                                                                  int8_t* __restrict__ q, long long ldq,
                                                                  float* __restrict__ scale) {
     __shared__ unsigned part[8];
+    griddep_wait();     // nothing is read or written before the kernel before this one has ended
+    griddep_launch();   // and the next one's blocks may come as soon as all of this one's have
     const T* xr = x + (long long)blockIdx.x * ldx;
     int8_t* qr = q + (long long)blockIdx.x * ldq;
     unsigned m = 0;
@@ -130,6 +132,8 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
     constexpr int N = 16 / sizeof(T);
     extern __shared__ __align__(16) uint8_t staged[];   // QT / G rows of room_of(K) bytes
     __shared__ unsigned part[QT / 32];
+    griddep_wait();     // nothing is read or written before the kernel before this one has ended
+    griddep_launch();   // and the next one's blocks may come as soon as all of this one's have
     const int t = threadIdx.x % G, in_block = threadIdx.x / G;
     const long long row = (long long)blockIdx.x * (QT / G) + in_block;
     const bool live = row < rows;
@@ -221,10 +225,10 @@ void launch_short(const Ctx& ctx, const T* x, long long ldx, int rows, int K, in
     const bool aligned = ((uintptr_t)x & 15) == 0 && ((uintptr_t)q & (N - 1)) == 0 && (ldx | ldq | K) % N == 0;
     const int grid = ceil_div(rows, QT / G);
     if (aligned)
-        quantize_rows_kernel<T, G, QT, true><<<grid, QT, 0, ctx.stream>>>(x, ldx, rows, K, q, ldq, scale);
+        launch_pdl(ctx, quantize_rows_kernel<T, G, QT, true>, dim3(grid), dim3(QT), 0, x, ldx, rows, K, q, ldq, scale);
     else
-        quantize_rows_kernel<T, G, QT, false><<<grid, QT, (QT / G) * ((K + 15 + 16 + 15) / 16 * 16), ctx.stream>>>(
-            x, ldx, rows, K, q, ldq, scale);
+        launch_pdl(ctx, quantize_rows_kernel<T, G, QT, false>, dim3(grid), dim3(QT),
+                   (size_t)(QT / G) * ((K + 15 + 16 + 15) / 16 * 16), x, ldx, rows, K, q, ldq, scale);
 }
 
 }  // namespace
@@ -241,7 +245,7 @@ void launch_quantize_rows(const Ctx& ctx, const T* x, long long ldx, int rows, i
     else if (vecs <= 256 * QV)
         launch_short<T, 256>(ctx, x, ldx, rows, K, q, ldq, scale);
     else
-        quantize_long_rows_kernel<T><<<rows, 256, 0, ctx.stream>>>(x, ldx, K, q, ldq, scale);
+        launch_pdl(ctx, quantize_long_rows_kernel<T>, dim3(rows), dim3(256), 0, x, ldx, K, q, ldq, scale);
     ++*ctx.launches;
 }
 

@@ -402,6 +402,8 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
     const int tid = threadIdx.x % NT, lane = tid & 31;
     const int row = CLUSTER ? blockIdx.x / parts : blockIdx.x * ROWS + threadIdx.x / NT;
     const int part = CLUSTER ? blockIdx.x % parts : 0;
+    griddep_wait();     // nothing is read or written before the kernel before this one has ended
+    griddep_launch();   // and the next one's blocks may come as soon as all of this one's have
     if (ROWS > 1 && row >= rows) return;
     const T* x = logits + (long long)row * ld;
     const RowVecs<T> rv(x, V);
@@ -543,6 +545,8 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, lo
                                                                  long long ldd, int parts, unsigned* status) {
     constexpr int N = RowVecs<T>::N, U = 4;
     const int row = blockIdx.x / parts, part = blockIdx.x % parts;
+    griddep_wait();     // nothing is read or written before the kernel before this one has ended
+    griddep_launch();   // and the next one's blocks may come as soon as all of this one's have
     const T* x = x0 + (long long)row * ld;
     T* dx = dx0 + (long long)row * ldd;
     int t = targets ? targets[row] : -1;
@@ -617,26 +621,16 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, lo
 template <typename T, int NT>
 void launch_rows(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float inv_tau, const int* targets,
                  const LogprobOut& out) {
-    token_logprobs_kernel<T, NT, false><<<ceil_div(rows, BLOCK_OF<NT> / NT), BLOCK_OF<NT>, 0, ctx.stream>>>(
-        logits, ld, rows, V, inv_tau, targets, out, 1, ctx.status);
+    launch_pdl(ctx, token_logprobs_kernel<T, NT, false>, dim3(ceil_div(rows, BLOCK_OF<NT> / NT)), dim3(BLOCK_OF<NT>), 0,
+               logits, ld, rows, V, inv_tau, targets, out, 1, ctx.status);
 }
 
 // A cluster of `parts` blocks of 128 threads a row.
 template <typename T>
 void launch_split(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float inv_tau, const int* targets,
                   const LogprobOut& out, int parts) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(rows * parts);
-    cfg.blockDim = dim3(128);
-    cfg.stream = ctx.stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = parts;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, 128, true>, logits, ld, rows, V, inv_tau, targets, out, parts,
-                       ctx.status);
+    launch_pdl_clusters(ctx, parts, token_logprobs_kernel<T, 128, true>, dim3(rows * parts), dim3(128), 0, logits, ld, rows,
+                        V, inv_tau, targets, out, parts, ctx.status);
 }
 
 }  // namespace
@@ -671,9 +665,8 @@ void launch_token_logprobs_bwd(const Ctx& ctx, const T* logits, long long ld, in
     int per = 16;
     while (per > 2 && (long long)rows * ceil_div(vecs, 256 * per) < 8 * ctx.num_sms) per /= 2;
     const int parts = ceil_div(vecs, 256 * per);
-    token_logprobs_bwd_kernel<T><<<rows * parts, 256, 0, ctx.stream>>>(logits, ld, V, 1.f / temperature, targets, lse,
-                                                                       dlogp, entropy, dentropy, dlogits, ldd, parts,
-                                                                       ctx.status);
+    launch_pdl(ctx, token_logprobs_bwd_kernel<T>, dim3(rows * parts), dim3(256), 0, logits, ld, V, 1.f / temperature, targets,
+               lse, dlogp, entropy, dentropy, dlogits, ldd, parts, ctx.status);
     ++*ctx.launches;
 }
 

@@ -211,6 +211,13 @@ extern "C" int gpt2k_embedding_bwd(const int32_t* idx, const float* dx, int B, i
 namespace {
 bool misaligned(const void* p, size_t bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
 size_t elem_size(int dtype) { return dtype == GPT2K_F32 ? 4 : 2; }
+// Programmatic dependent launch: the call's blocks start while the kernel before it in the stream ends,
+// and wait for it (griddep_wait) before they touch memory. About 1 us less between small calls.
+Ctx early_kctx(void* stream, uint32_t* status, long long* launches) {
+    Ctx c = kctx(stream, status, launches);
+    c.pdl = true;
+    return c;
+}
 constexpr int MAX_EXTENT = 1 << 30;   // rows, columns: 32-bit index arithmetic has room past them
 }  // namespace
 
@@ -224,7 +231,7 @@ extern "C" int gpt2k_quantize_rows(int dtype, const void* x, int rows, int K, in
     if (misaligned(x, elem_size(dtype)) || misaligned(scale, 4))
         return set_error(GPT2_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
     long long launches = 0;
-    Ctx c = kctx(stream, nullptr, &launches);
+    Ctx c = early_kctx(stream, nullptr, &launches);
     if (dtype == GPT2K_F32)
         launch_quantize_rows<float>(c, (const float*)x, ldx, rows, K, q, ldq, scale);
     else
@@ -256,7 +263,7 @@ extern "C" int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scal
         misaligned(bias, 4) || misaligned(resid, 4) || misaligned(status_dev, 4))
         return set_error(GPT2_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
     long long launches = 0;
-    Ctx c = kctx(stream, status_dev, &launches);
+    Ctx c = early_kctx(stream, status_dev, &launches);
     I8Product p;
     p.A = A;
     p.lda = lda;
@@ -316,7 +323,7 @@ extern "C" int gpt2k_token_logprobs(int dtype, const void* logits, int rows, int
         misaligned(top_ids, 4) || misaligned(top_logp, 4))
         return set_error(GPT2_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
     long long launches = 0;
-    Ctx c = kctx(stream, status_dev, &launches);
+    Ctx c = early_kctx(stream, status_dev, &launches);
     const LogprobOut o = {logp, entropy, lse, top_ids, top_logp, top_k};
     if (dtype == GPT2K_F32)
         launch_token_logprobs<float>(c, (const float*)logits, ld, rows, V, temperature, targets, o);
@@ -345,7 +352,7 @@ extern "C" int gpt2k_token_logprobs_bwd(int dtype, const void* logits, int rows,
         misaligned(dlogp, 4) || misaligned(entropy, 4) || misaligned(dentropy, 4))
         return set_error(GPT2_ERR_INVALID_ARG, "a pointer is not aligned to its element type");
     long long launches = 0;
-    Ctx c = kctx(stream, status_dev, &launches);
+    Ctx c = early_kctx(stream, status_dev, &launches);
     if (dtype == GPT2K_F32)
         launch_token_logprobs_bwd<float>(c, (const float*)logits, ld, rows, V, temperature, targets, lse, dlogp,
                                          entropy, dentropy, (float*)dlogits, ldd);

@@ -34,6 +34,25 @@ inline void launch_pdl(const Ctx& ctx, void (*kernel)(KArgs...), dim3 grid, dim3
     cfg.numAttrs = ctx.pdl ? 1 : 0;
     cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
+// The same in clusters of `cluster` blocks.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl_clusters(const Ctx& ctx, int cluster, void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                                       size_t smem, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = ctx.pdl ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
 
 // ----------------------------------------------------------------------------
 // GEMM epilogues. The contraction produces fp32 acc(row, col); the epilogue
