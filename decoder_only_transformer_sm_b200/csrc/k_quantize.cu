@@ -5,11 +5,16 @@
 //
 // q is the nearest whole number (ties to even) of the exact quotient, so the
 // codes do not depend on how the quotient is rounded: t = x * fl32(127 / a)
-// is within 2 * 2^-24 * 127 < 1.6e-5 of it, and only a t closer than 1.7e-5 to the
-// border between two codes is decided by a 64-bit division (there 127 x is
-// exact, and a quotient that is not a border differs from one by more than
-// 2^-41 relative, so rounding the division cannot make a tie). So are rows whose
-// largest value is below 1e-30, where 127 / a could overflow.
+// is within 2 * 2^-24 * 127 < 1.6e-5 of it, so its nearest whole number n is q or,
+// close to a border between two codes, q's neighbour, and e = 127 x - n a, compared
+// with a / 2, decides which. For bf16 x (8 bits) e is exact in fp32, and every vector is
+// checked by it: ties are common there (127 x / a with two 8-bit significands). For fp32 x
+// only a t closer than 1.7e-5 to a border is, with e as a sum of two fp32 numbers:
+// 127 x and n a each as a product and its rounding error (fma), whose differences are exact
+// that close to each other. 127 and a carry a power of two that keeps 127 x finite; rows
+// whose largest value is below 1e-30, where 127 / a could overflow, take the 64-bit quotient
+// (127 x is exact, and a quotient that is not a border differs from one by more than 2^-41
+// relative, so rounding the division cannot make a tie).
 //
 // Bound by memory: a row is read once, as 16-byte vectors that stay in registers
 // (up to 8 a thread) between the maximum and the codes. Rows may start at
@@ -27,44 +32,86 @@ namespace {
 constexpr float MAGIC = 12582912.f;   // 3 * 2^22
 constexpr float BORDER = 0.5f - 1.7e-5f;
 
-__device__ __noinline__ unsigned code_at_border(float x, float a) {
-    return (unsigned)(int)rint(127.0 * (double)x / (double)a) & 0xffu;
+// What a row's codes are made with.
+struct Step {
+    float a, inv;     // largest magnitude; 127 / a, or 0 where a is too small (or no number)
+    float c, as;      // 127 and a times the power of two
+    __device__ __forceinline__ explicit Step(float a_) : a(a_) {
+        inv = a > 1e-30f ? 127.f / a : 0.f;
+        const float s = a > 1e30f ? 0.00390625f : 1.f;
+        c = 127.f * s;
+        as = a * s;
+    }
+};
+
+// n (in the low bits of `code`) moved to its neighbour if e = 127 x - n a says so: d = |e| - a / 2.
+__device__ __forceinline__ void decide(unsigned& code, float e, float d) {
+    if (d > 0.f || (d == 0.f && (code & 1u))) code += e > 0.f ? 1u : ~0u;
 }
 
-// Codes of N values as N bytes: inv = 127 / a, 0 where that is no normal number (every
-// code is then taken from the 64-bit quotient; a = 0 gives 0).
-template <int N>
-__device__ __forceinline__ void codes(const float (&x)[N], float a, float inv, unsigned (&out)[N / 4]) {
-    unsigned c[N];
-    float off[N], far = 0.f;
-    const f32x2 i2 = pk2(inv, inv), up = pk2(MAGIC, MAGIC), down = pk2(-MAGIC, -MAGIC), minus = pk2(-1.f, -1.f);
+// Codes of N values as N bytes (inv is not 0).
+__device__ __forceinline__ void codes(const float (&x)[8], const Step& st, unsigned (&out)[2], bf16) {
+    unsigned c[8];
+    float e[8], far = 0.f;
+    const f32x2 i2 = pk2(st.inv, st.inv), up = pk2(MAGIC, MAGIC), down = pk2(MAGIC, MAGIC), a2 = pk2(st.as, st.as),
+                c2 = pk2(st.c, st.c), minus = pk2(-1.f, -1.f);
 #pragma unroll
-    for (int j = 0; j < N; j += 2) {
-        const f32x2 t = mul2(pk2(x[j], x[j + 1]), i2);
-        const f32x2 n = add2(t, up);
+    for (int j = 0; j < 8; j += 2) {
+        const f32x2 v = pk2(x[j], x[j + 1]);
+        const f32x2 n = add2(mul2(v, i2), up);
         float n0, n1;
         upk2(n, n0, n1);
-        upk2(fma2(add2(n, down), minus, t), off[j], off[j + 1]);
-        far = fmaxf(far, fmaxf(fabsf(off[j]), fabsf(off[j + 1])));
+        upk2(fma2(fma2(n, minus, down), a2, mul2(v, c2)), e[j], e[j + 1]);   // -n a + 127 x
+        far = fmaxf(far, fmaxf(fabsf(e[j]), fabsf(e[j + 1])));
         c[j] = __float_as_uint(n0);
         c[j + 1] = __float_as_uint(n1);
     }
-    if (far > BORDER || inv == 0.f) {
+    const float half = 0.5f * st.as;
+    if (far >= half) {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (fabsf(off[j]) > BORDER || inv == 0.f) c[j] = a > 0.f ? code_at_border(x[j], a) : 0u;
+        for (int j = 0; j < 8; ++j) decide(c[j], e[j], fabsf(e[j]) - half);
     }
 #pragma unroll
-    for (int j = 0; j < N; j += 4)
+    for (int j = 0; j < 8; j += 4)
         out[j / 4] = __byte_perm(__byte_perm(c[j], c[j + 1], 0x0040), __byte_perm(c[j + 2], c[j + 3], 0x0040), 0x5410);
 }
-__device__ __forceinline__ unsigned code(float x, float a, float inv) {
+__device__ __forceinline__ void codes(const float (&x)[4], const Step& st, unsigned (&out)[1], float) {
+    unsigned c[4];
+    float n[4], far = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float t = x[j] * st.inv, m = t + MAGIC;
+        n[j] = m - MAGIC;
+        far = fmaxf(far, fabsf(t - n[j]));
+        c[j] = __float_as_uint(m);
+    }
+    if (far > BORDER) {
+        const float half = 0.5f * st.as;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float p = x[j] * st.c, q = n[j] * st.as, e = p - q;
+            const float low = fmaf(x[j], st.c, -p) - fmaf(n[j], st.as, -q);
+            // e is within a rounding error of 127 x - n a, `low` is what it lacks
+            decide(c[j], e, (fabsf(e) - half) + (e > 0.f ? low : -low));
+        }
+    }
+    out[0] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+}
+// The code of one value, decided where it has to be by the 64-bit quotient (inv = 0: always).
+__device__ __noinline__ unsigned code(float x, float a, float inv) {
     const float t = x * inv, n = t + MAGIC;
-    if (fabsf(t - (n - MAGIC)) > BORDER || inv == 0.f) return a > 0.f ? code_at_border(x, a) : 0u;
+    if (fabsf(t - (n - MAGIC)) > BORDER || inv == 0.f)
+        return a > 0.f ? (unsigned)(int)rint(127.0 * (double)x / (double)a) & 0xffu : 0u;
     return __float_as_uint(n) & 0xffu;
 }
-// 127 / a, or 0 where a is so small (or no number) that the 64-bit quotient is taken.
-__device__ __forceinline__ float inverse(float a) { return a > 1e-30f ? 127.f / a : 0.f; }
+// A row whose inv is 0, value by value (read again, so that the pass over the others need not keep it).
+template <int N, int G, typename T>
+__device__ __forceinline__ void slow_codes(const T* x, int8_t* out, int t, int full, const Step& st) {
+    for (int i = t; i < full; i += G) {
+#pragma unroll 1
+        for (int j = 0; j < N; ++j) out[i * N + j] = (int8_t)code(to_f(x[i * N + j]), st.a, st.inv);
+    }
+}
 
 // The bits of |x| order like its value, with inf and NaN above every finite one.
 __device__ __forceinline__ unsigned magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
@@ -89,8 +136,8 @@ __global__ void __launch_bounds__(256) quantize_long_rows_kernel(const T* __rest
     for (int w = 1; w < 8; ++w) m = max(m, part[w]);
     const bool fine = m < 0x7f800000u;
     if (threadIdx.x == 0) scale[blockIdx.x] = fine ? __uint_as_float(m) / 127.f : __uint_as_float(0x7fc00000u);
-    const float a = fine ? __uint_as_float(m) : 0.f, inv = inverse(a);
-    for (int k = threadIdx.x; k < K; k += 256) qr[k] = (int8_t)code(to_f(xr[k]), a, inv);
+    const Step st(fine ? __uint_as_float(m) : 0.f);
+    for (int k = threadIdx.x; k < K; k += 256) qr[k] = (int8_t)code(to_f(xr[k]), st.a, st.inv);
 }
 
 __device__ __forceinline__ void unpack(const uint4& q, float (&f)[8], bf16) {
@@ -165,16 +212,20 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
     }
     const bool fine = m < 0x7f800000u;
     if (live && t == 0) scale[row] = fine ? __uint_as_float(m) / 127.f : __uint_as_float(0x7fc00000u);
-    const float a = fine ? __uint_as_float(m) : 0.f, inv = inverse(a);
+    const Step st(fine ? __uint_as_float(m) : 0.f);
     if (ALIGNED) {
         if (!live) return;
+        if (st.inv == 0.f) {
+            slow_codes<N, G>(xr, qr, t, full, st);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < QV; ++i) {
             if (t + i * G < full) {
                 float f[N];
                 unsigned c[N / 4];
                 unpack(v[i], f, T());
-                codes<N>(f, a, inv, c);
+                codes(f, st, c, T());
                 if (N == 8) *reinterpret_cast<uint2*>(qr + (t + i * G) * N) = make_uint2(c[0], c[N / 4 - 1]);
                 else *reinterpret_cast<unsigned*>(qr + (t + i * G) * N) = c[0];
             }
@@ -184,8 +235,8 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
     const int lead = (int)((uintptr_t)qr & 15);
     int8_t* room = reinterpret_cast<int8_t*>(staged) + in_block * ((K + 15 + 16 + 15) / 16 * 16) + lead;
     if (live) {
-        if (t < head) room[t] = (int8_t)code(h, a, inv);
-        if (t < tail) room[K - tail + t] = (int8_t)code(e, a, inv);
+        if (t < head) room[t] = (int8_t)code(h, st.a, st.inv);
+        if (t < tail) room[K - tail + t] = (int8_t)code(e, st.a, st.inv);
         const bool words = ((lead + head) & 3) == 0;
 #pragma unroll
         for (int i = 0; i < QV; ++i) {
@@ -193,7 +244,7 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
                 float f[N];
                 unsigned c[N / 4];
                 unpack(v[i], f, T());
-                codes<N>(f, a, inv, c);
+                codes(f, st, c, T());
                 int8_t* at = room + head + (t + i * G) * N;
 #pragma unroll
                 for (int j = 0; j < N / 4; ++j) {
@@ -206,6 +257,7 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
                 }
             }
         }
+        if (st.inv == 0.f) slow_codes<N, G>(xr + head, room + head, t, full, st);
     }
     if (G > 32) __syncthreads();
     else __syncwarp();

@@ -73,6 +73,34 @@ def test_quantize_rows(dtype, rows, K, pad_x, pad_q, shift):
     assert torch.all(whole[:, K:] == 77) and torch.all(room[:shift] == 77) and scale[rows] == 5.0
 
 
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -90, 2.0 ** 120, 2.0 ** -110])
+def test_codes_at_borders(scale):
+    """bf16: every significand of a row's largest value against every one of its elements over nine binades (with all
+    their ties). fp32: the numbers next to (2 k + 1) a / 254 on both sides, for many a."""
+    from decoder_only_transformer_sm_b200 import native
+    tops = (np.arange(128, 256) * 2.0 ** -7 * scale)[:, None]
+    x = (np.arange(128, 256)[:, None] * 2.0 ** (-7.0 - np.arange(9))).reshape(1, -1) * scale
+    x = np.where(x <= tops, x, 0.0)
+    rows = [np.concatenate([tops, x, -x], 1)]
+    rng = np.random.default_rng(1)
+    a = (rng.uniform(1.0, 2.0, 200) * scale).astype(np.float32)
+    near = ((2 * np.arange(127) + 1)[None, :] * a.astype(np.float64)[:, None] / 254.0).astype(np.float32)
+    up, down = np.nextafter(near, np.float32(np.inf)), np.nextafter(near, np.float32(0))
+    rows.append(np.concatenate([a[:, None], near, -near, up, -up, down, -down], 1).clip(-a[:, None], a[:, None]))
+    for v, dtype in zip(rows, (torch.bfloat16, torch.float32)):
+        dx = torch.from_numpy(v.astype(np.float32)).to(dtype).cuda()
+        assert np.array_equal(dx.float().cpu().numpy(), v.astype(np.float32))
+        R, K = dx.shape
+        for pad in (0, -K % 16 + 16):
+            q, s = torch.empty((R, K + pad), dtype=torch.int8, device="cuda"), torch.empty(R, device="cuda")
+            x_in = torch.zeros((R, K + pad), dtype=dtype, device="cuda")[:, :K]
+            x_in.copy_(dx)
+            native.quantize_rows(x_in, q[:, :K], s)
+            want_q, want_s = _codes64(v.astype(np.float32))
+            np.testing.assert_array_equal(q[:, :K].cpu().numpy(), want_q)
+            np.testing.assert_array_equal(s.cpu().numpy(), want_s)
+
+
 def _gelu64(u):
     return 0.5 * u * (1.0 + np.tanh(np.sqrt(2.0 / np.pi) * (u + 0.044715 * u ** 3)))
 

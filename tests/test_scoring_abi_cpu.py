@@ -89,10 +89,10 @@ def test_binding_refusals():
 
 
 def test_fp32_quotient_is_within_its_bound():
-    """For a > 1e-30 the kernel takes the code of t = fl(x fl(127 / a)), read from the low bits of fl(t + 3 2^22), unless
-    t lies within 1.7e-5 of a border, and decides those (and smaller a) by a 64-bit division: t has to be within 1.6e-5 of
-    the quotient (two roundings of half a step each, 127 * 2 * 2^-24 = 1.6e-5), and the quotient's 64-bit rounding
-    must not make or lose a tie."""
+    """For a > 1e-30 the kernel's first guess is the whole number nearest t = fl(x fl(127 / a)), read from the low bits
+    of fl(t + 3 2^22); fp32 rows look again at a t within 1.7e-5 of a border. t has to be within 1.6e-5 of the quotient
+    (two roundings of half a step each, 127 * 2 * 2^-24 = 1.5e-5), and a 64-bit quotient (smaller a) must not make or
+    lose a tie."""
     rng = np.random.default_rng(0)
     for scale in (1.0, 1e-26, 3e37):
         a = (np.abs(rng.standard_normal(200000)) * scale + scale * 1e-3).astype(np.float32)
