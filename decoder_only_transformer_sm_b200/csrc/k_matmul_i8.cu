@@ -159,6 +159,9 @@ void launch_rows(const Ctx& ctx, const I8Product& p) {
 // is a row), scale it and turn it around in shared memory, 32 rows of 128 bytes at a time, which leave
 // by a TMA store or as 16-byte stores of the warp (single elements where rows are not whole 16-byte segments). Rows and columns past the operands come as zeros from TMA and are not stored.
 // Rows that start anywhere (BYTES): eight more warps take the place of the TMA loads.
+// Of tiles up to 128 columns two threads issue the MMAs, every other K block each: one gets one MMA
+// per 120 cycles or so through, however narrow it is. Their two sums are added in the epilogue (128 x 768
+// x 6400: 14.8 us, with one thread 18.3; then a CTA's 55 bytes a cycle of loads bound it).
 // A pair shares its B rows, so a K block costs each CTA 32 KB of shared memory and of L2
 // traffic for 256 x 256 outputs a pair, where one CTA alone needs 48 KB for 128 x 256.
 template <int BN, int CTAS, bool BYTES = false>
@@ -166,12 +169,13 @@ struct Tile {
     static constexpr int BM = 128, BK = 128;   // rows of a CTA
     static constexpr int B_ROWS = BN / CTAS;   // B rows in a CTA's shared memory
     static constexpr int A_BYTES = BM * BK, B_BYTES = B_ROWS * BK, STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = BN >= 128 ? 5 : 8;
+    static constexpr int STAGES = BN >= 256 ? 5 : BN >= 128 ? 4 : 8;   // even where two threads issue MMAs
     static constexpr int EPI_WARPS = BN >= 256 ? 16 : BN >= 128 ? 8 : 4;
     static constexpr int BYTE_WARPS = BYTES ? 8 : 0;
-    static constexpr int THREADS = 64 + 32 * (EPI_WARPS + BYTE_WARPS);
+    static constexpr int ISSUERS = BN <= 128 ? 2 : 1;    // threads that issue MMAs, each into a sum of its own
+    static constexpr int THREADS = 32 * (1 + ISSUERS + EPI_WARPS + BYTE_WARPS);
     static constexpr int WCOLS = BN / (EPI_WARPS / 4);   // columns of a warp
-    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int TMEM_COLS = 2 * ISSUERS * BN;
     static constexpr int EPI_BUFS = BN >= 256 ? 1 : 2;   // a warp's staging buffers
     static constexpr int EPI_COLS = 8 * BN;              // bytes of the tile's column scales and biases
 };
@@ -350,10 +354,10 @@ __global__ void __launch_bounds__(Tile<BN, CTAS, BYTES>::THREADS, 1)
             tc::mbar_init(&ctl->empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            tc::mbar_init(&ctl->acc_full[b], 1);
+            tc::mbar_init(&ctl->acc_full[b], L::ISSUERS);
             tc::mbar_init(&ctl->acc_empty[b], CTAS * L::EPI_WARPS);
         }
-        tc::mbar_init(&ctl->drain, 1);
+        tc::mbar_init(&ctl->drain, L::ISSUERS);
         ctl->abort = 0;
         tc::fence_barrier_init();
     }
@@ -375,7 +379,8 @@ __global__ void __launch_bounds__(Tile<BN, CTAS, BYTES>::THREADS, 1)
     const uint32_t tmem = ctl->tmem_base;
     griddep_launch();
 
-    if (BYTES && warp >= 2 + L::EPI_WARPS) {
+    constexpr int LAST = 2 + L::EPI_WARPS + L::BYTE_WARPS;   // the second issuing warp
+    if (BYTES && warp >= 2 + L::EPI_WARPS && warp < LAST) {
         const int bw = warp - 2 - L::EPI_WARPS;
         uint32_t it = 0, ok = 1;
         for (int u = first; u < tiles && ok; u += step) {
@@ -447,8 +452,12 @@ __global__ void __launch_bounds__(Tile<BN, CTAS, BYTES>::THREADS, 1)
                 }
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == LAST) {
         if (lane == 0 && rank == 0) {
+            // Every other K block of the CTA's whole run, so that a stage is always the same thread's: one that saw
+            // only every other phase of a barrier could take an old one's parity for its own.
+            const uint32_t mine = warp == 1 ? 0 : 1;
+            static_assert(L::ISSUERS == 1 || L::STAGES % L::ISSUERS == 0, "a stage belongs to one issuing thread");
             constexpr uint32_t idesc = tc::idesc_i8_s32(L::BM * CTAS, BN);
             uint32_t it = 0, acc_it = 0;
             bool ok = true;
@@ -456,8 +465,10 @@ __global__ void __launch_bounds__(Tile<BN, CTAS, BYTES>::THREADS, 1)
                 const uint32_t ab = acc_it & 1;
                 if (!tc::mbar_wait(&ctl->acc_empty[ab], ((acc_it >> 1) & 1) ^ 1, abort, status)) break;
                 tc::fence_after_sync();
-                const uint32_t d_tmem = tmem + ab * BN;
+                const uint32_t d_tmem = tmem + (ab * L::ISSUERS + mine) * BN;
+                uint32_t add = 0;   // the tile's first MMA overwrites
                 for (int kb = 0; kb < grid.k_blocks; ++kb, ++it) {
+                    if (L::ISSUERS > 1 && it % L::ISSUERS != mine) continue;
                     const int s = it % L::STAGES;
                     if (!tc::mbar_wait(&ctl->full[s], (it / L::STAGES) & 1, abort, status)) {
                         ok = false;
@@ -469,8 +480,9 @@ __global__ void __launch_bounds__(Tile<BN, CTAS, BYTES>::THREADS, 1)
                     for (int kk = 0; kk < L::BK / 32; ++kk) {
                         const uint64_t da = tc::smem_desc_sw128(a_base + kk * 32, 16, 1024);
                         const uint64_t db = tc::smem_desc_sw128(a_base + L::A_BYTES + kk * 32, 16, 1024);
-                        if (PAIR) tc::mma_i8_pair(d_tmem, da, db, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-                        else tc::mma_i8(d_tmem, da, db, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                        if (PAIR) tc::mma_i8_pair(d_tmem, da, db, idesc, add);
+                        else tc::mma_i8(d_tmem, da, db, idesc, add);
+                        add = 1;
                     }
                     if (PAIR) tc::mma_commit_pair(&ctl->empty[s]);
                     else tc::mma_commit(&ctl->empty[s]);
@@ -550,7 +562,7 @@ __global__ void __launch_bounds__(Tile<BN, CTAS, BYTES>::THREADS, 1)
                     else tc::mbar_arrive(&ctl->acc_empty[ab]);
                 }
             };
-            const uint32_t taddr = tmem + ab * BN + cbase + ((uint32_t)(quarter * 32) << 16);
+            const uint32_t taddr = tmem + ab * L::ISSUERS * BN + cbase + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll
             for (int c0 = 0; c0 < L::WCOLS; c0 += CW, ++chunk) {
                 if (n0 + c0 >= p.N || row0 >= p.M) break;
@@ -559,7 +571,16 @@ __global__ void __launch_bounds__(Tile<BN, CTAS, BYTES>::THREADS, 1)
 #pragma unroll
                 for (int h = 0; h < CW; h += 32) {
                     float acc[32];
-                    tc::tmem_ld_32x32b_x32(taddr + c0 + h, acc);
+                    if (L::ISSUERS > 1 && grid.k_blocks > 1) {
+                        float more[32];
+                        tc::tmem_ld2_32x32b_x32(taddr + c0 + h, taddr + BN + c0 + h, acc, more);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            acc[i] = __int_as_float(__float_as_int(acc[i]) + __float_as_int(more[i]));
+                    } else {   // one K block: the sum of the thread whose turn it was
+                        const uint32_t of = L::ISSUERS > 1 ? acc_it % L::ISSUERS : 0;
+                        tc::tmem_ld_32x32b_x32(taddr + of * BN + c0 + h, acc);
+                    }
 #pragma unroll
                     for (int c = 0; c < 32; c += PER) {
                         uint8_t* at = buf + seg(lane, (h + c) / PER);
@@ -697,18 +718,18 @@ bool launch_kind(const Ctx& ctx, const I8Product& p) {
             return true;
         }
         // The tile width by its time: a start, then for each round of tiles over the SMs the K blocks and what
-        // of the epilogue the next tile's products do not cover. One MMA takes its issuing thread 120-170 cycles
-        // whatever its width, so a K block costs narrow tiles hardly less; they win while they fill SMs that wide
-        // ones leave idle. (us, measured with both operands in L2 over 64 .. 4096 rows: 64 x 2304 x 768 5.0 with
-        // 64 columns, 5.2 with 128, 7.2 with a pair; 1024 x 2304 x 768 7.4, 5.9, 8.2; 256 x 50304 x 768 26.8, 18.4, 14.2.)
+        // of the epilogue the next tile's products do not cover. A K block costs narrow tiles hardly less (their A
+        // rows are as many, and an MMA of few columns takes as long to issue); they win while they fill SMs that
+        // wide ones leave idle. (us, measured with both operands in L2: 64 x 2304 x 768 4.4 with 64 columns, 7.2
+        // with a pair; 1024 x 2304 x 768 7.4 with 64, 5.4 with 128, 8.2 with a pair; 256 x 50304 x 768 26.8, 18.4, 14.2.)
         const int kb = ceil_div(p.K, 128);
         auto time = [&](int bm, int bn, int units, float start, float block, float tile) {
             const float tiles = (float)ceil_div(p.M, bm) * (float)ceil_div(p.N, bn);
             return start + ceilf(tiles / units) * (kb * block + tile);
         };
         const float t256 = time(256, 256, ctx.num_sms / 2, 3.9f, 0.36f, 1.1f);
-        const float t128 = time(128, 128, ctx.num_sms, 2.6f, 0.32f, 0.7f);
-        const float t64 = time(128, 64, ctx.num_sms, 2.5f, 0.30f, 0.6f);
+        const float t128 = time(128, 128, ctx.num_sms, 2.5f, 0.26f, 0.7f);
+        const float t64 = time(128, 64, ctx.num_sms, 2.4f, 0.24f, 0.6f);
         if (t256 <= t128 && t256 <= t64) return launch_tc<KIND, O, 256, 2>(ctx, p);
         return t128 <= t64 ? launch_tc<KIND, O, 128, 1>(ctx, p) : launch_tc<KIND, O, 64, 1>(ctx, p);
     }
