@@ -5,10 +5,10 @@
 // The sum is a 32-bit integer, exact for K <= 131071 (128^2 K < 2^31); it is
 // rounded once to fp32 and multiplied by sa[m], then sb[n], in fp32.
 //
-// Three kernels, chosen by the shape and the alignment of the operands:
-//   M <= 8, 16-byte rows   weight streaming (below): bound by reading B once
+// Chosen by the shape and the alignment of the operands:
+//   M <= 8                 weight streaming (k_matmul_i8_rows.cu): bound by reading B once
 //   M > 8, 16-byte rows    tcgen05 (kind::i8) with TMA operands
-//   other strides          tcgen05 with operands that warps put together from bytes
+//   M > 8, other rows      tcgen05 with operands that warps put together from aligned words
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -21,18 +21,8 @@ namespace gpt2 {
 
 namespace {
 
-// One scaled sum through the epilogue. GELU in the tanh form for fp32 results
-// and in the logistic form for bf16 ones (gelu_for).
-template <int KIND, typename O>
-__device__ __forceinline__ O finish(int acc, float sa, float sb, float bias, float resid) {
-    float u = ((float)acc * sa) * sb;
-    if (KIND != EPI_STORE) u += bias;
-    if (KIND == EPI_BIAS_GELU) u = gelu_for<O>(u);
-    if (KIND == EPI_BIAS_RESID) u += resid;
-    return from_f<O>(u);
-}
-
-// Two at a time, in packed arithmetic (the same operations and roundings).
+// Two scaled sums through the epilogue, in packed arithmetic. GELU in the tanh form for fp32 results and
+// in the logistic form for bf16 ones, as gelu_for.
 template <int KIND, typename O>
 __device__ __forceinline__ f32x2 finish2(int a0, int a1, f32x2 sa, f32x2 sb, f32x2 bias, f32x2 resid) {
     f32x2 u = mul2(pk2((float)a0, (float)a1), sa);
@@ -52,103 +42,6 @@ __device__ __forceinline__ f32x2 finish2(int a0, int a1, f32x2 sa, f32x2 sb, f32
         }
     }
     return u;
-}
-
-// ---------------------------------------------------------------- few rows
-// Weight streaming for M <= MM rows: each warp takes RG rows of B at a time, a lane 16
-// bytes of each per step (two steps in flight); the matching bytes of the M rows of A come from
-// L1. Lane r * MM + m finishes element (m, n0 + r); its scales are requested first, so that a
-// warp's life is about one trip to memory.
-constexpr int GV_M = 8, GV_THREADS = 128;
-
-// The last bytes of a row, K % 16 of them, and zeros: what follows a row belongs to nobody.
-__device__ __forceinline__ int4 load_tail(const int8_t* row, int K) {
-    int w[4] = {0, 0, 0, 0};
-    for (int i = 0; i < (K & 15); ++i) w[i >> 2] |= (row[(K & ~15) + i] & 0xff) << (8 * (i & 3));
-    return make_int4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ int dot16(int4 a, int4 b, int acc) {
-    return __dp4a(a.w, b.w, __dp4a(a.z, b.z, __dp4a(a.y, b.y, __dp4a(a.x, b.x, acc))));
-}
-
-template <int KIND, typename O, int MM, int RG>
-__global__ void __launch_bounds__(GV_THREADS) matmul_i8_rows_kernel(I8Product p) {
-    const int lane = threadIdx.x & 31;
-    const int n0 = (blockIdx.x * (GV_THREADS / 32) + (threadIdx.x >> 5)) * RG;
-    griddep_wait();     // nothing is read or written before the kernel before this one has ended
-    griddep_launch();   // and the next one's blocks may come as soon as all of this one's have
-    if (n0 >= p.N) return;
-    const int chunks = p.K / 16;
-    const int4* b[RG];
-#pragma unroll
-    for (int r = 0; r < RG; ++r)
-        b[r] = reinterpret_cast<const int4*>(p.B + (long long)min(n0 + r, p.N - 1) * p.ldb);
-    const int4* a[MM];
-#pragma unroll
-    for (int m = 0; m < MM; ++m)
-        a[m] = reinterpret_cast<const int4*>(p.A + (long long)min(m, p.M - 1) * p.lda);
-    const int my_m = lane % MM, my_n = n0 + lane / MM;
-    const bool mine = lane < RG * MM && my_m < p.M && my_n < p.N;
-    float sa = 0.f, sb = 0.f, bias = 0.f, resid = 0.f;
-    int acc[RG][MM] = {};
-    for (int j0 = lane; j0 < chunks; j0 += 64) {
-        int4 w[2][RG];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int r = 0; r < RG; ++r)
-                w[u][r] = j0 + 32 * u < chunks ? __ldg(b[r] + j0 + 32 * u) : make_int4(0, 0, 0, 0);
-        if (j0 == lane && mine) {
-            sa = __ldg(p.sa + my_m);
-            sb = __ldg(p.sb + my_n);
-            if (KIND != EPI_STORE) bias = __ldg(p.bias + my_n);
-            if (KIND == EPI_BIAS_RESID) resid = p.resid[(long long)my_m * p.ldr + my_n];
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            int4 x[MM];
-#pragma unroll
-            for (int m = 0; m < MM; ++m) x[m] = j0 + 32 * u < chunks ? __ldg(a[m] + j0 + 32 * u) : make_int4(0, 0, 0, 0);
-#pragma unroll
-            for (int m = 0; m < MM; ++m)
-#pragma unroll
-                for (int r = 0; r < RG; ++r) acc[r][m] = dot16(x[m], w[u][r], acc[r][m]);
-        }
-    }
-    if (lane >= chunks && mine) {   // a lane that the loop above passed by
-        sa = __ldg(p.sa + my_m);
-        sb = __ldg(p.sb + my_n);
-        if (KIND != EPI_STORE) bias = __ldg(p.bias + my_n);
-        if (KIND == EPI_BIAS_RESID) resid = p.resid[(long long)my_m * p.ldr + my_n];
-    }
-    if ((p.K & 15) && lane == 0) {
-#pragma unroll
-        for (int r = 0; r < RG; ++r) {
-            const int4 w = load_tail(reinterpret_cast<const int8_t*>(b[r]), p.K);
-#pragma unroll
-            for (int m = 0; m < MM; ++m)
-                acc[r][m] = dot16(load_tail(reinterpret_cast<const int8_t*>(a[m]), p.K), w, acc[r][m]);
-        }
-    }
-    int sum = 0;
-#pragma unroll
-    for (int r = 0; r < RG; ++r)
-#pragma unroll
-        for (int m = 0; m < MM; ++m) {
-            const int t = __reduce_add_sync(0xffffffffu, acc[r][m]);
-            if (lane == r * MM + m) sum = t;
-        }
-    if (mine) reinterpret_cast<O*>(p.out)[(long long)my_m * p.ldo + my_n] = finish<KIND, O>(sum, sa, sb, bias, resid);
-}
-
-template <int KIND, typename O, int MM>
-void launch_rows(const Ctx& ctx, const I8Product& p) {
-    // four rows a warp once that leaves every SM eight warps, else one
-    constexpr int W = GV_THREADS / 32;
-    if (p.N >= 4 * 8 * ctx.num_sms)
-        launch_pdl(ctx, matmul_i8_rows_kernel<KIND, O, MM, 4>, dim3(ceil_div(p.N, 4 * W)), dim3(GV_THREADS), 0, p);
-    else
-        launch_pdl(ctx, matmul_i8_rows_kernel<KIND, O, MM, 1>, dim3(ceil_div(p.N, W)), dim3(GV_THREADS), 0, p);
 }
 
 // ---------------------------------------------------------------- tensor cores
@@ -273,61 +166,66 @@ __device__ __forceinline__ void put(uint8_t* at, const f32x2 (&v)[4], bf16) {
     *reinterpret_cast<uint4*>(at) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// 16 bytes from k on of a row of K that starts at any byte, zeros past its end. lo .. hi: the
-// bytes of the whole operand; 32-bit words that touch others are put together from single bytes.
-__device__ __forceinline__ uint4 gather16(const int8_t* row, int k, int K, const int8_t* lo, const int8_t* hi) {
-    unsigned w[4] = {0, 0, 0, 0};
-    const int8_t* at = row + k;
-    const int off = (int)((uintptr_t)at & 3);
-    const unsigned* word = reinterpret_cast<const unsigned*>(at - off);
-    if (k + 16 <= K && at - off >= lo && at - off + 20 <= hi) {
-        unsigned u[5];
-#pragma unroll
-        for (int i = 0; i < 5; ++i) u[i] = __ldg(word + i);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(u[i], u[i + 1], 8 * off);
-    } else {
-        for (int i = 0; i < min(16, K - k); ++i) w[i >> 2] |= (unsigned)(uint8_t)at[i] << (8 * (i & 3));
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// One warp's part of a K block of 128 rows from row0 on, in the 128-byte-swizzle layout that TMA
-// writes: 16-byte pieces, four a lane. A block that is not the first along K and has 132 bytes left touches
-// no word outside the operand (rows past it are read as its last one, and not stored), so all its loads go
-// out before the first store; `edge` looks at each piece.
+// One warp's part of a K block of 128 rows from row0 on of an operand whose rows start at any
+// byte, in the 128-byte-swizzle layout that TMA writes: pieces of 16 bytes, four a lane, each put
+// together from five aligned 32-bit words, all loads before the first store. Rows past the
+// operand are read as its last one (and not stored). EDGE: the first K block, and those near the
+// rows' end: what lies past K counts as zero, and the pieces whose words would touch a byte outside
+// the operand (at its first and its last byte only) are put together from single bytes.
 struct Gather {
     const int8_t* base;
     long long ld;
     int row0, rows;
     static constexpr int PIECES = 128 * 8 / (8 * 32);   // 8 warps
-    __device__ __forceinline__ void load(unsigned (&u)[PIECES][5], int (&off)[PIECES], int k0, int i0) const {
+    struct Words {
+        unsigned u[PIECES][5];
+    };
+    __device__ __forceinline__ const int8_t* piece(int i, int k0) const {
+        return base + (long long)min(row0 + (i >> 3), rows - 1) * ld + k0 + 16 * (i & 7);
+    }
+    __device__ __forceinline__ bool inside(const int8_t* word, int K) const {
+        return word >= base && word + 20 <= base + (long long)(rows - 1) * ld + K;
+    }
+    template <bool EDGE>
+    __device__ __forceinline__ void load(Words& w, int k0, int K, int i0) const {
 #pragma unroll
         for (int j = 0; j < PIECES; ++j) {
             const int i = i0 + 256 * j;
-            const int8_t* at = base + (long long)min(row0 + (i >> 3), rows - 1) * ld + k0 + 16 * (i & 7);
-            off[j] = (int)((uintptr_t)at & 3);
-            const unsigned* word = reinterpret_cast<const unsigned*>(at - off[j]);
+            const int8_t* at = piece(i, k0);
+            const int8_t* word = at - ((uintptr_t)at & 3);
+            const bool ok = !EDGE || inside(word, K);
 #pragma unroll
-            for (int w = 0; w < 5; ++w) u[j][w] = __ldg(word + w);
+            for (int x = 0; x < 5; ++x) w.u[j][x] = ok ? __ldg(reinterpret_cast<const unsigned*>(word) + x) : 0u;
         }
     }
-    __device__ __forceinline__ void store(uint8_t* dst, const unsigned (&u)[PIECES][5], const int (&off)[PIECES], int i0) const {
+    template <bool EDGE>
+    __device__ __forceinline__ void store(uint8_t* dst, const Words& w, int k0, int K, int i0) const {
 #pragma unroll
         for (int j = 0; j < PIECES; ++j) {
-            const int i = i0 + 256 * j, sh = 8 * off[j];
-            *reinterpret_cast<uint4*>(dst + seg(i >> 3, i & 7)) =
-                make_uint4(__funnelshift_r(u[j][0], u[j][1], sh), __funnelshift_r(u[j][1], u[j][2], sh),
-                           __funnelshift_r(u[j][2], u[j][3], sh), __funnelshift_r(u[j][3], u[j][4], sh));
-        }
-    }
-    __device__ __forceinline__ void edge(uint8_t* dst, int k0, int K, int i0) const {
-        const int8_t* hi = base + (long long)(rows - 1) * ld + K;
+            const int i = i0 + 256 * j;
+            const int8_t* at = piece(i, k0);
+            const int off = (int)((uintptr_t)at & 3);
+            unsigned q[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) q[x] = __funnelshift_r(w.u[j][x], w.u[j][x + 1], 8 * off);
+            if (EDGE) {
+                const int left = K - (k0 + 16 * (i & 7));   // bytes of the row from here on
+                if (left > 0 && !inside(at - off, K)) {
+                    q[0] = q[1] = q[2] = q[3] = 0;
 #pragma unroll 1
-        for (int j = 0; j < PIECES; ++j) {
-            const int i = i0 + 256 * j, r = row0 + (i >> 3), k = k0 + 16 * (i & 7);
-            *reinterpret_cast<uint4*>(dst + seg(i >> 3, i & 7)) =
-                r < rows && k < K ? gather16(base + (long long)r * ld, k, K, base, hi) : make_uint4(0, 0, 0, 0);
+                    for (int b = 0; b < min(left, 16); ++b) {
+                        const unsigned v = (unsigned)(uint8_t)at[b] << (8 * (b & 3));
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) q[x] |= (b >> 2) == x ? v : 0u;
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int n = left - 4 * x;
+                    q[x] = n >= 4 ? q[x] : n <= 0 ? 0u : q[x] & ((1u << (8 * n)) - 1);
+                }
+            }
+            *reinterpret_cast<uint4*>(dst + seg(i >> 3, i & 7)) = make_uint4(q[0], q[1], q[2], q[3]);
         }
     }
 };
@@ -394,16 +292,17 @@ __global__ void __launch_bounds__(Tile<BN, CTAS, BYTES>::THREADS, 1)
                 uint8_t* sa = smem + s * L::STAGE_BYTES;
                 const Gather ga = {p.A, p.lda, mb * L::BM, p.M}, gb = {p.B, p.ldb, nb * BN, p.N};
                 const int k0 = kb * L::BK, i0 = bw * 32 + lane;
-                if (kb > 0 && k0 + 132 <= p.K) {
-                    unsigned ua[Gather::PIECES][5], ub[Gather::PIECES][5];
-                    int oa[Gather::PIECES], ob[Gather::PIECES];
-                    ga.load(ua, oa, k0, i0);
-                    gb.load(ub, ob, k0, i0);
-                    ga.store(sa, ua, oa, i0);
-                    gb.store(sa + L::A_BYTES, ub, ob, i0);
+                Gather::Words wa, wb;
+                if (kb > 0 && k0 + 132 <= p.K) {   // (a piece's last word may reach three bytes past it)
+                    ga.load<false>(wa, k0, p.K, i0);
+                    gb.load<false>(wb, k0, p.K, i0);
+                    ga.store<false>(sa, wa, k0, p.K, i0);
+                    gb.store<false>(sa + L::A_BYTES, wb, k0, p.K, i0);
                 } else {
-                    ga.edge(sa, k0, p.K, i0);
-                    gb.edge(sa + L::A_BYTES, k0, p.K, i0);
+                    ga.load<true>(wa, k0, p.K, i0);
+                    gb.load<true>(wb, k0, p.K, i0);
+                    ga.store<true>(sa, wa, k0, p.K, i0);
+                    gb.store<true>(sa + L::A_BYTES, wb, k0, p.K, i0);
                 }
                 tc::fence_proxy_async_smem();   // the MMA reads through the async proxy
                 __syncwarp();
@@ -707,16 +606,8 @@ bool launch_tc(const Ctx& ctx, const I8Product& p) {
 }
 
 template <int KIND, typename O>
-bool launch_kind(const Ctx& ctx, const I8Product& p) {
-    ++*ctx.launches;
-    if (whole_segments(p.A, p.lda, 1) && whole_segments(p.B, p.ldb, 1)) {
-        if (p.M <= GV_M) {
-            if (p.M == 1) launch_rows<KIND, O, 1>(ctx, p);
-            else if (p.M == 2) launch_rows<KIND, O, 2>(ctx, p);
-            else if (p.M <= 4) launch_rows<KIND, O, 4>(ctx, p);
-            else launch_rows<KIND, O, 8>(ctx, p);
-            return true;
-        }
+bool launch_kind(const Ctx& ctx, const I8Product& p, bool whole) {
+    if (whole) {
         // The tile width by its time: a start, then for each round of tiles over the SMs the K blocks and what
         // of the epilogue the next tile's products do not cover. A K block costs narrow tiles hardly less (their A
         // rows are as many, and an MMA of few columns takes as long to issue); they win while they fill SMs that
@@ -739,12 +630,18 @@ bool launch_kind(const Ctx& ctx, const I8Product& p) {
 }  // namespace
 
 bool launch_matmul_i8(const Ctx& ctx, const I8Product& p) {
+    ++*ctx.launches;
+    const bool whole = whole_segments(p.A, p.lda, 1) && whole_segments(p.B, p.ldb, 1), f32 = p.out_f32;
+    if (p.M <= I8_FEW_ROWS) {
+        launch_matmul_i8_rows(ctx, p, whole);
+        return true;
+    }
     switch (p.kind) {
-    case EPI_STORE: return p.out_f32 ? launch_kind<EPI_STORE, float>(ctx, p) : launch_kind<EPI_STORE, bf16>(ctx, p);
-    case EPI_BIAS: return p.out_f32 ? launch_kind<EPI_BIAS, float>(ctx, p) : launch_kind<EPI_BIAS, bf16>(ctx, p);
+    case EPI_STORE: return f32 ? launch_kind<EPI_STORE, float>(ctx, p, whole) : launch_kind<EPI_STORE, bf16>(ctx, p, whole);
+    case EPI_BIAS: return f32 ? launch_kind<EPI_BIAS, float>(ctx, p, whole) : launch_kind<EPI_BIAS, bf16>(ctx, p, whole);
     case EPI_BIAS_GELU:
-        return p.out_f32 ? launch_kind<EPI_BIAS_GELU, float>(ctx, p) : launch_kind<EPI_BIAS_GELU, bf16>(ctx, p);
-    case EPI_BIAS_RESID: return launch_kind<EPI_BIAS_RESID, float>(ctx, p);
+        return f32 ? launch_kind<EPI_BIAS_GELU, float>(ctx, p, whole) : launch_kind<EPI_BIAS_GELU, bf16>(ctx, p, whole);
+    case EPI_BIAS_RESID: return launch_kind<EPI_BIAS_RESID, float>(ctx, p, whole);
     default: return false;
     }
 }

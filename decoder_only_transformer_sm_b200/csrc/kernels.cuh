@@ -304,7 +304,7 @@ void launch_copy_tokens(const Ctx& ctx, const int* src, long long src_ld, int* d
                         int cols);
 
 // ----------------------------------------------------------------------------
-// 8-bit linear layers (k_quantize.cu, k_matmul_i8.cu) and token log-probabilities
+// 8-bit linear layers (k_quantize.cu, k_matmul_i8.cu, k_matmul_i8_rows.cu) and token log-probabilities
 // (k_token_logprobs.cu).
 // ----------------------------------------------------------------------------
 // Row r of x (rows x K, stride ldx) -> int8 codes q (stride ldq) and scale[r]; the
@@ -332,7 +332,10 @@ struct I8Product {
     long long ldr;
 };
 constexpr int I8_MAX_K = 131071;   // (2^31 - 1) / 128^2: every sum fits in 32 bits
+constexpr int I8_FEW_ROWS = 8;
 bool launch_matmul_i8(const Ctx& ctx, const I8Product& p);
+// M <= I8_FEW_ROWS; whole: rows of A and B are whole 16-byte segments.
+void launch_matmul_i8_rows(const Ctx& ctx, const I8Product& p, bool whole);
 
 // Results of gpt2k_token_logprobs; NULL members are not computed.
 struct LogprobOut {
