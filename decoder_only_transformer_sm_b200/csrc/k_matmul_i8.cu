@@ -53,7 +53,8 @@ __device__ __forceinline__ f32x2 finish2(int a0, int a1, f32x2 sa, f32x2 sb, f32
 // ring of STAGES; warp 1 (of the pair's first CTA) issues tcgen05.mma (kind::i8, 128 CTAS x BN x 32)
 // into one of two int32 accumulators in tensor memory; the epilogue warps read the other one (a lane
 // is a row), scale it and turn it around in shared memory, 32 rows of 128 bytes at a time, which leave
-// by a TMA store or as 16-byte stores of the warp (single elements where rows are not whole 16-byte segments). Rows and columns past the operands come as zeros from TMA and are not stored.
+// by a TMA store or as 16-byte stores of the warp (single elements where rows are not whole 16-byte
+// segments). Rows and columns past the operands come as zeros from TMA and are not stored.
 // Rows that start anywhere (BYTES): eight more warps take the place of the TMA loads.
 // Of tiles up to 128 columns two threads issue the MMAs, every other K block each: one gets one MMA
 // per 120 cycles or so through, however narrow it is. Their two sums are added in the epilogue (128 x 768

@@ -59,7 +59,6 @@ __global__ void __launch_bounds__(GV_THREADS) matmul_i8_rows_kernel(I8Product p)
     const int lane = threadIdx.x & 31;
     const int n0 = (blockIdx.x * (GV_THREADS / 32) + (threadIdx.x >> 5)) * RG;
     griddep_wait();     // nothing is read or written before the kernel before this one has ended
-    griddep_launch();   // and the next one's blocks may come as soon as all of this one's have
     if (n0 >= p.N) return;
     const int chunks = p.K / 16;
     const int8_t* b[RG];
@@ -102,6 +101,7 @@ __global__ void __launch_bounds__(GV_THREADS) matmul_i8_rows_kernel(I8Product p)
                 for (int r = 0; r < RG; ++r) acc[r][m] = dot16(x[m], w[u][r], acc[r][m]);
         }
     }
+    griddep_launch();   // the next kernel's blocks may come: not earlier, they would crowd on the SMs with room
     if (lane >= chunks && mine) {   // a lane that the loop above passed by
         sa = __ldg(p.sa + my_m);
         sb = __ldg(p.sb + my_n);

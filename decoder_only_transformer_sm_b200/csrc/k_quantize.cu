@@ -124,7 +124,6 @@ __global__ void __launch_bounds__(256) quantize_long_rows_kernel(const T* __rest
                                                                  float* __restrict__ scale) {
     __shared__ unsigned part[8];
     griddep_wait();     // nothing is read or written before the kernel before this one has ended
-    griddep_launch();   // and the next one's blocks may come as soon as all of this one's have
     const T* xr = x + (long long)blockIdx.x * ldx;
     int8_t* qr = q + (long long)blockIdx.x * ldq;
     unsigned m = 0;
@@ -135,6 +134,7 @@ __global__ void __launch_bounds__(256) quantize_long_rows_kernel(const T* __rest
     m = part[0];
 #pragma unroll
     for (int w = 1; w < 8; ++w) m = max(m, part[w]);
+    griddep_launch();   // the next kernel's blocks may come: not earlier, they would crowd on the SMs with room
     const bool fine = m < 0x7f800000u;
     if (threadIdx.x == 0) scale[blockIdx.x] = fine ? __uint_as_float(m) / 127.f : __uint_as_float(0x7fc00000u);
     const Step st(fine ? __uint_as_float(m) : 0.f);
@@ -181,7 +181,6 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
     extern __shared__ __align__(16) uint8_t staged[];   // QT / G rows of room_of(K) bytes
     __shared__ unsigned part[QT / 32];
     griddep_wait();     // nothing is read or written before the kernel before this one has ended
-    griddep_launch();   // and the next one's blocks may come as soon as all of this one's have
     const int t = threadIdx.x % G, in_block = threadIdx.x / G;
     const long long row = (long long)blockIdx.x * (QT / G) + in_block;
     const bool live = row < rows;
@@ -211,6 +210,7 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
 #pragma unroll
         for (int w = 1; w < G / 32; ++w) m = max(m, part[in_block * (G / 32) + w]);
     }
+    griddep_launch();   // the next kernel's blocks may come: not earlier, they would crowd on the SMs with room
     const bool fine = m < 0x7f800000u;
     if (live && t == 0) scale[row] = fine ? __uint_as_float(m) / 127.f : __uint_as_float(0x7fc00000u);
     const Step st(fine ? __uint_as_float(m) : 0.f);

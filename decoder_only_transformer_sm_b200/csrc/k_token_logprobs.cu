@@ -310,16 +310,14 @@ __device__ __forceinline__ void find_top(ForwardSmem<NT>& sm, const T* x, const 
     const unsigned bound = sm.bound;
     const int steps = ceil_div(end - begin, NT), n_again = sm.n_again;
     if (n_again <= 2 * top_k) {
-        const float bound_value = value_of(bound), per_step = 1.f / steps;
+        const float bound_value = value_of(bound);   // NaN for a bound of 0, which everything reaches
         constexpr int R = 2;
         for (int k0 = tid; k0 < n_again * steps; k0 += R * NT) {
             uint4 q[R];
             int at[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                // vector k % steps of thread again[k / steps] (k + 1/2 is off a whole multiple by more than the
-                // product's rounding: k < 2^21)
-                const int k = k0 + r * NT, g = (int)((k + 0.5f) * per_step);
+                const int k = k0 + r * NT, g = k / steps;   // vector k % steps of thread again[g]
                 at[r] = g < n_again ? begin + (k - g * steps) * NT + sm.again[g] : end;
                 q[r] = at[r] < end ? load_vec(x, rv, at[r], end) : make_uint4(0, 0, 0, 0);
             }
@@ -404,7 +402,6 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
     const int row = CLUSTER ? blockIdx.x / parts : blockIdx.x * ROWS + threadIdx.x / NT;
     const int part = CLUSTER ? blockIdx.x % parts : 0;
     griddep_wait();     // nothing is read or written before the kernel before this one has ended
-    griddep_launch();   // and the next one's blocks may come as soon as all of this one's have
     if (ROWS > 1 && row >= rows) return;
     const T* x = logits + (long long)row * ld;
     const RowVecs<T> rv(x, V);
@@ -505,6 +502,7 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
         keys = cs.top;
         n_keys = parts * out.top_k;
     }
+    griddep_launch();   // the next kernel's blocks may come: not earlier, they would crowd on the SMs with room
     const float z_max = a.m * inv_tau;
     const bool bad = a.s != a.s || z_max == -NEG_INF, empty = !bad && (a.s == 0.f || z_max == NEG_INF);
     const float log_s = logf(a.s);
@@ -548,7 +546,6 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, lo
     constexpr int N = RowVecs<T>::N, U = 4;
     const int row = blockIdx.x / parts, part = blockIdx.x % parts;
     griddep_wait();     // nothing is read or written before the kernel before this one has ended
-    griddep_launch();   // and the next one's blocks may come as soon as all of this one's have
     const T* x = x0 + (long long)row * ld;
     T* dx = dx0 + (long long)row * ldd;
     int t = targets ? targets[row] : -1;
@@ -569,6 +566,7 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, lo
     uint4* to = reinterpret_cast<uint4*>(dx + rv.head);
     const int i0 = part * per + threadIdx.x;
     if (none) {
+        griddep_launch();
         for (int i = i0; i < end; i += 256) {
             if (i < rv.full) to[i] = make_uint4(0, 0, 0, 0);
             else scatter_vec(dx, rv, i, make_uint4(0, 0, 0, 0));
@@ -601,8 +599,8 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, lo
                 float d0, d1, y0, y1;
                 upk2(d2, d0, d1);
                 upk2(mul2(d2, e2), y0, y1);
-                // a masked value: p = 0, d = -inf
-                const f32x2 f2 = fma2(B2, pk2(fmaxf(d0, -1e30f), fmaxf(d1, -1e30f)), A2);
+                // where p is 0 (d below -104, -inf where masked) its factor need only be finite
+                const f32x2 f2 = fma2(B2, pk2(fmaxf(d0, -128.f), fmaxf(d1, -128.f)), A2);
                 upk2(mul2(pk2(ex2_approx(y0), ex2_approx(y1)), f2), r[j], r[j + 1]);
             }
             const int at = t - rv.first(k);
@@ -617,6 +615,7 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, lo
 #pragma unroll
         for (int u = 0; u < U; ++u) q[u] = next[u];
     }
+    griddep_launch();   // the next kernel's blocks may come: not earlier, they would crowd on the SMs with room
 }
 
 // NT threads a row.

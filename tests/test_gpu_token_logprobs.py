@@ -199,6 +199,28 @@ def test_one_element_at_every_place():
         assert np.array_equal(o["ids"][:, 0], np.arange(V))
 
 
+@pytest.mark.parametrize("rows", [1, 297])
+def test_long_rows(rows):
+    """A vocabulary of millions: one row over a cluster, many a block each."""
+    from decoder_only_transformer_sm_b200 import native
+    V = 20_000_003 if rows == 1 else 1_000_001
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn((rows, V), generator=g, device="cuda")
+    lse, H = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    ids, top = torch.empty((rows, 32), dtype=torch.int32, device="cuda"), torch.empty((rows, 32), device="cuda")
+    native.token_logprobs(x, V, 1.0, lse=lse, entropy=H, top_ids=ids, top_logp=top)
+    for r in range(0, rows, 74):
+        logp = torch.log_softmax(x[r].double(), 0)
+        best = torch.sort(x[r], descending=True, stable=True).indices[:32]
+        assert torch.equal(ids[r].long(), best)
+        # V / 128 + 16 additions in a row at 2^-24 (V / 1024 over a cluster), exp's 2^-21
+        tol = (V / (1024 if rows == 1 else 256) + 16) * EPS + 2.0 ** -21 + 40 * EPS
+        assert (top[r].double() - logp[best]).abs().max() <= tol
+        assert abs(float(lse[r].double() - torch.logsumexp(x[r].double(), 0))) <= tol
+        want = float(-(logp.exp() * logp).sum())
+        assert abs(float(H[r]) - want) <= 2 * (want + 3) * tol
+
+
 def test_bad_targets_are_reported():
     from decoder_only_transformer_sm_b200 import native
     V = 50
