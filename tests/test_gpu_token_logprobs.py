@@ -475,3 +475,50 @@ def test_side_stream_and_graphs():
             graph.replay()
         for j, (loss, _) in enumerate(made):
             assert all(torch.equal(a, b) for a, b in zip(loss.results(), want[i + j]))
+
+
+def test_calls_at_once_on_two_streams():
+    """An 8-bit product, quantisation and log-probabilities on one stream beside the same on another: each gets what
+    it gets alone."""
+    from decoder_only_transformer_sm_b200 import native
+    gen = torch.Generator().manual_seed(3)
+
+    class Work:
+        def __init__(self, M, N, K, V):
+            self.x = torch.randn((M, K), generator=gen).to(torch.bfloat16).cuda()
+            self.q, self.s = torch.empty((M, K), dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+            self.w = torch.randint(-127, 128, (N, K), generator=gen, dtype=torch.int8).cuda()
+            self.ws = torch.rand(N, generator=gen).cuda() * 1e-3
+            self.out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+            self.V = V
+            self.H, self.lse = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+            self.ids, self.top = torch.empty((M, 9), dtype=torch.int32, device="cuda"), torch.empty((M, 9), device="cuda")
+            self.d = torch.empty_like(self.out)
+            self.g = torch.rand(M, generator=gen).cuda()
+            self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+        def run(self, stream=None):
+            native.quantize_rows(self.x, self.q, self.s, stream=stream)
+            native.matmul_i8(self.q, self.s, self.w, self.ws, self.out, status=self.status, stream=stream)
+            native.token_logprobs(self.out, self.V, 0.9, lse=self.lse, entropy=self.H, top_ids=self.ids,
+                                  top_logp=self.top, status=self.status, stream=stream)
+            native.token_logprobs_bwd(self.out, self.V, 0.9, self.lse, self.d, entropy=self.H, dentropy=self.g,
+                                      status=self.status, stream=stream)
+
+        def results(self):
+            return [v.clone() for v in (self.q, self.s, self.out, self.H, self.lse, self.ids, self.top, self.d[:, :self.V])]
+
+    works = [Work(1500, 9000, 512, 8999), Work(40, 30000, 768, 29990), Work(5, 50304, 768, 50257), Work(300, 1000, 99, 1000)]
+    want = []
+    for w in works:
+        w.run()
+        want.append(w.results())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in works]
+    for _ in range(10):
+        for w, s in zip(works, streams):
+            w.run(stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    for w, r in zip(works, want):
+        assert int(w.status.item()) == 0
+        assert all(torch.equal(a, b) for a, b in zip(w.results(), r))
