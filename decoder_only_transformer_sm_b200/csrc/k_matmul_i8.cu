@@ -142,14 +142,23 @@ __device__ __forceinline__ void move_rows(uint8_t* buf, E* mem, long long ld, in
         }
         return;
     }
-    for (int r = 0; r < 32 && row0 + r < M; ++r) {
+    // rows that start anywhere: an element a lane, eight rows loaded before the first is stored
+#pragma unroll 1
+    for (int e = lane; e < COLS; e += 32) {
+        if (col0 + e >= N) continue;
+        E* g = mem + (long long)row0 * ld + col0 + e;
+        uint8_t* at = buf + (e % PER) * sizeof(E);
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += 8) {
+            E t[8];
 #pragma unroll
-        for (int e = lane; e < COLS; e += 32) {
-            if (col0 + e >= N) continue;
-            E* g = mem + (long long)(row0 + r) * ld + col0 + e;
-            E* s = reinterpret_cast<E*>(buf + seg(r, e / PER)) + e % PER;
-            if (STORE) *g = *s;
-            else *s = *g;
+            for (int r = 0; r < 8; ++r)
+                if (row0 + r0 + r < M)
+                    t[r] = STORE ? *reinterpret_cast<const E*>(at + seg(r0 + r, e / PER)) : g[(r0 + r) * ld];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (row0 + r0 + r < M)
+                    *(STORE ? g + (r0 + r) * ld : reinterpret_cast<E*>(at + seg(r0 + r, e / PER))) = t[r];
         }
     }
 }

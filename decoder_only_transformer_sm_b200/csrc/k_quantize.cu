@@ -17,7 +17,7 @@
 // relative, so rounding the division cannot make a tie).
 //
 // Bound by memory: a row is read once, as 16-byte vectors that stay in registers
-// (up to 8 a thread) between the maximum and the codes. Rows may start at
+// (up to 8 a thread, 8 to 256 threads a row) between the maximum and the codes. Rows may start at
 // any element and codes at any byte: the elements before a row's first 16-byte boundary
 // and after its last one are held one a thread, and the codes go through shared memory,
 // laid out there like the memory they go to, so that they leave in 16-byte stores too. Where
@@ -202,7 +202,12 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
         for (int i = 0; i < QV; ++i) m = larger(m, v[i], T());
         m = max(whole(m, T()), max(magnitude(h), magnitude(e)));
     }
-    m = __reduce_max_sync(0xffffffffu, m);
+    if (G < 32) {
+#pragma unroll
+        for (int o = G / 2; o; o /= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    } else {
+        m = __reduce_max_sync(0xffffffffu, m);
+    }
     if (G > 32) {
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
         __syncthreads();
@@ -267,8 +272,8 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
         const int first = (16 - lead) & 15, last = max(first, K - ((lead + K) & 15));
         for (int k = first + 16 * t; k + 16 <= last; k += 16 * G)
             *reinterpret_cast<uint4*>(qr + k) = *reinterpret_cast<const uint4*>(room + k);
-        if (t < min(first, K)) qr[t] = room[t];
-        if (t < K - last) qr[last + t] = room[last + t];
+        for (int k = t; k < min(first, K); k += G) qr[k] = room[k];
+        for (int k = last + t; k < K; k += G) qr[k] = room[k];
     }
 }
 
@@ -291,7 +296,9 @@ void launch_quantize_rows(const Ctx& ctx, const T* x, long long ldx, int rows, i
                           float* scale) {
     // the fewest threads a row that hold it in registers
     const int vecs = K / (16 / (int)sizeof(T));
-    if (vecs <= 32 * QV)
+    if (vecs <= 32)   // eight: four rows a warp
+        launch_short<T, 8>(ctx, x, ldx, rows, K, q, ldq, scale);
+    else if (vecs <= 32 * QV)
         launch_short<T, 32>(ctx, x, ldx, rows, K, q, ldq, scale);
     else if (vecs <= 128 * QV)
         launch_short<T, 128>(ctx, x, ldx, rows, K, q, ldq, scale);
