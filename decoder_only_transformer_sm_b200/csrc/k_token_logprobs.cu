@@ -16,8 +16,10 @@
 // knows its largest value at the end, and the top_k-th largest of those is a bound that
 // at least top_k values of the row reach. Only threads that reach it can hold one of the
 // top_k: what they read is read again (from L2), and the few values that reach the bound
-// are ranked by 64-bit keys (value, then lowest index). Where more reach it than there is
-// room for (many equal ones), each warp instead keeps a sorted list while it reads again.
+// are ranked by 64-bit keys (value, then lowest index). Where many values equal the bound, only
+// the larger ones are gathered, and the first equal ones in the row's order after them; the
+// same way -inf fills up where fewer than top_k threads saw a number. (Where even the larger
+// ones are too many, a few threads holding most of a row's largest values, each warp keeps a sorted list.)
 // 8192 x 50257 bf16: 135 us without alternatives (6.1 TB/s), 153 with five, 229 with 32.
 #include <cooperative_groups.h>
 
@@ -235,6 +237,7 @@ struct ForwardSmem {
     u64 cand[ROOM];                       // keys that reach the bound (the warps' lists: NT at most)
     Sums sums[NT / 32];
     int again[NT];                        // the threads whose values are read again
+    int scan[NT / 32];
     unsigned bound;
     int n_cand, n_again;
 };
@@ -260,57 +263,106 @@ __device__ __forceinline__ void for_top(const u64* keys, int n, int k, int nt, F
 // Alternatives up to which a warp finds the bound by walking down from the largest value.
 constexpr int WALK = 8;
 
-// Leaves in sm.cand (sm.n_cand of them, visible to the threads of the row) keys among which
-// are the largest top_k of the vectors begin .. end - 1. any_nan: there is NaN or +inf.
-template <typename T, int NT>
-__device__ __forceinline__ void find_top(ForwardSmem<NT>& sm, const T* x, const RowVecs<T>& rv, int begin, int end,
-                                         int top_k, bool any_nan) {
+constexpr unsigned ORDER_NEG_INF = 0x007fffffu;   // order_of(-inf)
+
+    // Adds to sm.cand the first `need` (at most 32) values of this order among the vectors begin .. end - 1,
+// in the order of the row. (Like `lists` a function of its own: rarely needed, and registers.)
+    template <typename T, int NT>
+__device__ __noinline__ void fill(ForwardSmem<NT>& sm, const T* x, const RowVecs<T> rv, int begin, int end, unsigned order,
+                                  int need) {
     constexpr int N = RowVecs<T>::N, PER = NT / 32;
-    const int tid = threadIdx.x % NT, lane = tid & 31, warp = tid >> 5;
-    if (top_k <= WALK || NT == 32) {
-        if (warp == 0) {
-            unsigned key[PER], bound = 0xffffffffu;
+        const int tid = threadIdx.x % NT, lane = tid & 31, n0 = sm.n_cand;
+        const int head = end > rv.full ? rv.head : 0, from = rv.head + min(begin, rv.full) * N - head;
+        const int total = head + max(0, min(end, rv.full) - begin) * N +
+                          (end > rv.full + 1 ? rv.V - (rv.head + rv.full * N) : 0);
+        int found = 0;
+        for (int e0 = 0; e0 < total && found < need; e0 += NT * 8) {
+            unsigned hit = 0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) key[i] = sm.largest[lane + 32 * i];
-            // distinct values from the largest on, until top_k threads have reached them
-            for (int n = 0; n < top_k && bound != 0;) {
-                unsigned below = 0;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) below = max(below, key[i] < bound ? key[i] : 0u);
-                bound = __reduce_max_sync(0xffffffffu, below);
-#pragma unroll
-                for (int i = 0; i < PER; ++i) n += __popc(__ballot_sync(0xffffffffu, key[i] == bound));
+            for (int j = 0; j < 8; ++j) {
+                const int e = e0 + tid * 8 + j;
+                if (e < total && order_of(to_f(x[e < head ? e : from + e])) == order) hit |= 1u << j;
             }
-            int n = 0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const unsigned in = __ballot_sync(0xffffffffu, key[i] >= bound);
-                if ((in >> lane) & 1) sm.again[n + __popc(in & ((1u << lane) - 1))] = lane + 32 * i;
-                n += __popc(in);
+            int before = __popc(hit);   // of this and the lanes before, then of all threads before
+            for (int o = 1; o < 32; o *= 2) {
+                const int v = __shfl_up_sync(0xffffffffu, before, o);
+                if (lane >= o) before += v;
             }
-            if (lane == 0) {
-                sm.bound = bound;
-                sm.n_again = n;
+            if (lane == 31) sm.scan[tid >> 5] = before;
+            before -= __popc(hit);
+            meet<NT>();
+            int all = 0;
+            for (int w = 0; w < PER; ++w) {
+                if (w < (tid >> 5)) before += sm.scan[w];
+                all += sm.scan[w];
             }
+            for (int rank = found + before; hit && rank < need; hit &= hit - 1, ++rank) {
+                const int e = e0 + tid * 8 + __ffs(hit) - 1;
+                sm.cand[n0 + rank] = key_of(order, e < head ? e : from + e);
+            }
+            found += all;
+            meet<NT>();
         }
-    } else {   // every thread counts those above its own
-        const unsigned mine = sm.largest[tid];
-        int above = 0;
-#pragma unroll 8
-        for (int j = 0; j < NT; j += 4) {
-            const uint4 g = *reinterpret_cast<const uint4*>(sm.largest + j);
-            above += (g.x > mine) + (g.y > mine) + (g.z > mine) + (g.w > mine);
-        }
-        if (above < top_k) {
-            atomicMin(&sm.bound, mine);
-            sm.again[atomicAdd(&sm.n_again, 1)] = tid;
+        if (tid == 0) sm.n_cand = n0 + min(found, need);
+        meet<NT>();
+    }
+
+// Leaves in sm.cand the top_k of the chosen threads' values that reach `bound`, of each warp's threads.
+template <typename T, int NT>
+__device__ __noinline__ void lists(ForwardSmem<NT>& sm, const T* x, const RowVecs<T> rv, int begin, int end, unsigned bound,
+                                   int top_k) {
+    constexpr int N = RowVecs<T>::N, PER = NT / 32;
+    const int tid = threadIdx.x % NT, lane = tid & 31, n_again = sm.n_again;
+    u64 list = 0;
+    // 32 lanes read a thread's vectors of STEPS steps
+    constexpr int STEPS = 32 / N;
+    for (int g = tid >> 5; g < n_again; g += PER) {
+        const int mine = sm.again[g], j = lane % N;
+        for (int i0 = begin; i0 < end; i0 += STEPS * NT) {
+            const int i = i0 + lane / N * NT + mine;
+            const int e = i < end ? rv.first(i) + j : 0;
+            const bool is = i < end && e < rv.last(i);
+            const unsigned o = is ? order_of(to_f(x[e])) : 0u;
+            const u64 k = key_of(o, e);
+            // at most top_k of the list can be among the row's
+            const u64 least = __shfl_sync(0xffffffffu, list, top_k - 1);
+            insert(list, k, is && o >= bound && k > least);
         }
     }
+    const unsigned kept = __ballot_sync(0xffffffffu, list != 0 && lane < top_k);
+    int base = 0;
+    if (lane == 0 && kept) base = atomicAdd(&sm.n_cand, __popc(kept));
+    base = __shfl_sync(0xffffffffu, base, 0);
+    if ((kept >> lane) & 1) sm.cand[base + __popc(kept & ((1u << lane) - 1))] = list;
     meet<NT>();
-    const unsigned bound = sm.bound;
-    const int steps = ceil_div(end - begin, NT), n_again = sm.n_again;
-    if (n_again <= 2 * top_k) {
-        const float bound_value = value_of(bound);   // NaN for a bound of 0, which everything reaches
+}
+
+// The vectors begin .. end - 1 of a row, for one row's threads.
+template <typename T, int NT>
+struct Part {
+    ForwardSmem<NT>& sm;
+    const T* x;
+    const RowVecs<T>& rv;
+    int begin, end;
+    static constexpr int N = RowVecs<T>::N, PER = NT / 32;
+
+    // sm.again, sm.n_again: the threads whose largest value reaches `bound` (n_again is 0, all have met).
+    __device__ __forceinline__ void choose(unsigned bound) {
+        const int tid = threadIdx.x % NT;
+        if (sm.largest[tid] >= bound) sm.again[atomicAdd(&sm.n_again, 1)] = tid;
+        meet<NT>();
+    }
+    __device__ __forceinline__ void forget() {   // the candidates and the threads chosen
+        meet<NT>();
+        if (threadIdx.x % NT == 0) sm.n_cand = sm.n_again = 0;
+        meet<NT>();
+    }
+
+    // Adds the keys of the chosen threads' values that reach `bound` to sm.cand, as far as there is room;
+    // sm.n_cand counts them all.
+    __device__ __forceinline__ void gather(unsigned bound, bool any_nan) {
+        const int tid = threadIdx.x % NT, steps = ceil_div(end - begin, NT), n_again = sm.n_again;
+        const float bound_value = value_of(bound);
         constexpr int R = 2;
         for (int k0 = tid; k0 < n_again * steps; k0 += R * NT) {
             uint4 q[R];
@@ -341,50 +393,79 @@ __device__ __forceinline__ void find_top(ForwardSmem<NT>& sm, const T* x, const 
             }
         }
         meet<NT>();
-        if (sm.n_cand <= sm.ROOM) return;
-        meet<NT>();
-        if (tid == 0) sm.n_cand = 0;
-        meet<NT>();
     }
-    u64 list = 0;
-    // 32 lanes read a thread's vectors of STEPS steps
-    constexpr int STEPS = 32 / N;
-    for (int g = warp; g < n_again; g += PER) {
-        const int mine = sm.again[g], j = lane % N;
-        constexpr int R = 8;
-        for (int i0 = begin; i0 < end; i0 += R * STEPS * NT) {
-            float v[R];
-            int at[R];
+
+    // Leaves in sm.cand (sm.n_cand of them, visible to the threads of the row) keys among which are the
+    // part's top_k (all of them, if it has fewer values). any_nan: there is NaN or +inf.
+    __device__ __forceinline__ void find_top(int top_k, bool any_nan) {
+        const int tid = threadIdx.x % NT, lane = tid & 31;
+        if (top_k <= WALK || NT == 32) {
+            if (tid < 32) {
+                unsigned key[PER], bound = 0xffffffffu;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int i = i0 + (r * STEPS + lane / N) * NT + mine;
-                at[r] = -1;
-                v[r] = 0.f;
-                if (i < end) {
-                    const int e = rv.first(i) + j;
-                    if (e < rv.last(i)) {
-                        at[r] = e;
-                        v[r] = to_f(x[e]);
-                    }
+                for (int i = 0; i < PER; ++i) key[i] = sm.largest[lane + 32 * i];
+                // distinct values from the largest on, until top_k threads have reached them
+                for (int n = 0; n < top_k && bound > ORDER_NEG_INF;) {
+                    unsigned below = 0;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) below = max(below, key[i] < bound ? key[i] : 0u);
+                    bound = __reduce_max_sync(0xffffffffu, below);
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) n += __popc(__ballot_sync(0xffffffffu, key[i] == bound));
+                }
+                bound = max(bound, ORDER_NEG_INF + 1);
+                int n = 0;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const unsigned in = __ballot_sync(0xffffffffu, key[i] >= bound);
+                    if ((in >> lane) & 1) sm.again[n + __popc(in & ((1u << lane) - 1))] = lane + 32 * i;
+                    n += __popc(in);
+                }
+                if (lane == 0) {
+                    sm.bound = bound;
+                    sm.n_again = n;
                 }
             }
-#pragma unroll 1
-            for (int r = 0; r < R; ++r) {
-                const unsigned o = order_of(v[r]);
-                const u64 k = key_of(o, at[r]);
-                // at most top_k of the list can be among the row's
-                const u64 least = __shfl_sync(0xffffffffu, list, top_k - 1);
-                insert(list, k, at[r] >= 0 && o >= bound && k > least);
+        } else {   // every thread counts those above its own
+            const unsigned mine = sm.largest[tid];
+            int above = 0;
+#pragma unroll 8
+            for (int j = 0; j < NT; j += 4) {
+                const uint4 g = *reinterpret_cast<const uint4*>(sm.largest + j);
+                above += (g.x > mine) + (g.y > mine) + (g.z > mine) + (g.w > mine);
+            }
+            if (above < top_k && mine > ORDER_NEG_INF) {
+                atomicMin(&sm.bound, mine);
+                sm.again[atomicAdd(&sm.n_again, 1)] = tid;
             }
         }
+        meet<NT>();
+        const int n_again = sm.n_again;
+        const bool few = n_again < top_k;   // threads that saw a number: all their numbers count
+        const unsigned bound = few ? ORDER_NEG_INF + 1 : sm.bound;
+        bool fits = n_again <= 2 * top_k || n_again * ceil_div(end - begin, NT) * N <= sm.ROOM;
+        if (fits) {
+            gather(bound, any_nan);
+            fits = sm.n_cand <= sm.ROOM;
+        }
+        if (!fits && !few) {   // many equal to the bound
+            forget();
+            choose(bound + 1);
+            gather(bound + 1, any_nan);
+            if (sm.n_cand <= sm.ROOM) {
+                if (sm.n_cand < top_k) fill<T, NT>(sm, x, rv, begin, end, bound, top_k - sm.n_cand);
+                return;
+            }
+        }
+        if (!fits) {
+            forget();
+            choose(bound);
+            lists<T, NT>(sm, x, rv, begin, end, bound, top_k);
+        } else if (few && sm.n_cand < top_k) {
+            fill<T, NT>(sm, x, rv, begin, end, ORDER_NEG_INF, top_k - sm.n_cand);
+        }
     }
-    const unsigned kept = __ballot_sync(0xffffffffu, list != 0 && lane < top_k);
-    int base = 0;
-    if (lane == 0 && kept) base = atomicAdd(&sm.n_cand, __popc(kept));
-    base = __shfl_sync(0xffffffffu, base, 0);
-    if ((kept >> lane) & 1) sm.cand[base + __popc(kept & ((1u << lane) - 1))] = list;
-    meet<NT>();
-}
+};
 
 // Threads of a block: rows of a warp share one.
 template <int NT>
@@ -482,7 +563,7 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
             __syncwarp();
         }
     }
-    if (out.top_k && (CLUSTER || a.s != 0.f)) find_top<T, NT>(sm, x, rv, begin, end, out.top_k, a.s != a.s);
+    if (out.top_k && (CLUSTER || a.s != 0.f)) Part<T, NT>{sm, x, rv, begin, end}.find_top(out.top_k, a.s != a.s);
     const u64* keys = sm.cand;
     int n_keys = out.top_k ? sm.n_cand : 0;
     if constexpr (CLUSTER) {

@@ -23,7 +23,7 @@ pytestmark = pytest.mark.gpu
 
 EPS = 2.0 ** -24
 KINDS = ["normal", "equal", "up", "down", "empty", "one_left", "lowest", "half_masked", "nan", "inf", "few_values",
-         "peak", "signed_zeros"]
+         "peak", "signed_zeros", "few_left", "crowded", "ties"]
 
 
 def _rows(kinds, V, dtype, seed):
@@ -55,6 +55,18 @@ def _rows(kinds, V, dtype, seed):
             x[r] = rng.integers(0, 3, V)
         elif kind == "peak":
             x[r, V // 2] = 60.0
+        elif kind == "few_left":                            # fewer than the alternatives asked for
+            keep = np.array([0, V // 2, V - 1])
+            v = x[r, keep]
+            x[r] = -np.inf
+            x[r, keep] = v
+        elif kind == "crowded":                             # the largest values all with a few threads
+            x[r] *= 0.1
+            i = np.arange(V)
+            x[r] = np.where(i // 8 % 128 < 3, 5.0 + 4.0 * i / V, x[r])
+        elif kind == "ties":                                # three larger values, then hundreds of equal ones
+            x[r] = np.minimum(x[r], 2.0)
+            x[r, [V // 5, V // 4, V - 1]] = [7.0, 9.0, 8.0]
         elif kind == "signed_zeros":
             x[r] = np.where(rng.random(V) < 0.5, 0.0, -0.0)
     return torch.from_numpy(x).to(dtype)
