@@ -23,6 +23,8 @@
 // 8192 x 50257 bf16: 135 us without alternatives (6.1 TB/s), 153 with five, 229 with 32.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "kernels.cuh"
 
 namespace gpt2 {
@@ -613,25 +615,26 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
 
 // dx_v = (1/tau) [ g (1[v = t] - p_v) - h p_v (log p_v + H) ], g = dlogp (0 at an ignored
 // target), h = dentropy; with d = z_v - lse: p = e^d, and where p is 0 only the target's g is
-// left. One pass, bound by reading x and writing dx; a block takes a run of vectors of a row.
+// left. One pass, bound by reading x and writing dx; NT threads take a run of vectors of a row,
+// a block of at least 128 threads the runs of 128 / NT rows.
 // dx may be x: a thread writes only what it has read. 4096 x 50257 bf16, a quarter of the rows
 // not read: 124 us (5.8 TB/s).
-template <typename T>
-__global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, long long ld, int V, float inv_tau,
-                                                                 const int* __restrict__ targets,
-                                                                 const float* __restrict__ lse,
-                                                                 const float* __restrict__ dlogp,
-                                                                 const float* __restrict__ entropy,
-                                                                 const float* __restrict__ dentropy, T* dx0,
-                                                                 long long ldd, int parts, unsigned* status) {
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT < 128 ? 128 : NT)
+    token_logprobs_bwd_kernel(const T* x0, long long ld, int rows, int V, float inv_tau,
+                              const int* __restrict__ targets, const float* __restrict__ lse,
+                              const float* __restrict__ dlogp, const float* __restrict__ entropy,
+                              const float* __restrict__ dentropy, T* dx0, long long ldd, int parts, unsigned* status) {
     constexpr int N = RowVecs<T>::N, U = 4;
-    const int row = blockIdx.x / parts, part = blockIdx.x % parts;
+    constexpr int ROWS = NT < 128 ? 128 / NT : 1;
+    const int row = blockIdx.x / parts * ROWS + threadIdx.x / NT, part = blockIdx.x % parts, lane = threadIdx.x % NT;
     griddep_wait();     // nothing is read or written before the kernel before this one has ended
+    if (row >= rows) return;
     const T* x = x0 + (long long)row * ld;
     T* dx = dx0 + (long long)row * ldd;
     int t = targets ? targets[row] : -1;
     if (t < -1 || t >= V) {
-        if (threadIdx.x == 0) atomicOr(status, STATUS_BAD_TOKEN);
+        if (lane == 0) atomicOr(status, STATUS_BAD_TOKEN);
         t = min(max(t, 0), V - 1);
     }
     const float L = lse[row];
@@ -645,10 +648,10 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, lo
     const int whole = (((uintptr_t)x ^ (uintptr_t)dx) & 15) == 0 ? min(end, rv.full) : 0;
     const uint4* from = reinterpret_cast<const uint4*>(x + rv.head);
     uint4* to = reinterpret_cast<uint4*>(dx + rv.head);
-    const int i0 = part * per + threadIdx.x;
+    const int i0 = part * per + lane;
     if (none) {
         griddep_launch();
-        for (int i = i0; i < end; i += 256) {
+        for (int i = i0; i < end; i += NT) {
             if (i < rv.full) to[i] = make_uint4(0, 0, 0, 0);
             else scatter_vec(dx, rv, i, make_uint4(0, 0, 0, 0));
         }
@@ -657,7 +660,7 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, lo
     auto load = [&](uint4 (&q)[U], int i) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = i + u * 256;
+            const int k = i + u * NT;
             if (k < whole) q[u] = from[k];
             else if (k < end) q[u] = gather_vec(x, rv, k, end);
         }
@@ -665,12 +668,12 @@ __global__ void __launch_bounds__(256) token_logprobs_bwd_kernel(const T* x0, lo
     const f32x2 it2 = pk2(inv_tau, inv_tau), l2 = pk2(-L, -L), e2 = pk2(LOG2E, LOG2E), A2 = pk2(A, A), B2 = pk2(B, B);
     uint4 q[U];
     load(q, i0);
-    for (int i = i0; i < end; i += U * 256) {
+    for (int i = i0; i < end; i += U * NT) {
         uint4 next[U];
-        load(next, i + U * 256);
+        load(next, i + U * NT);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = i + u * 256;
+            const int k = i + u * NT;
             if (k >= end) break;
             float r[N];
             unpack(q[u], r, T());
@@ -742,13 +745,23 @@ template <typename T>
 void launch_token_logprobs_bwd(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float temperature,
                                const int* targets, const float* lse, const float* dlogp, const float* entropy,
                                const float* dentropy, T* dlogits, long long ldd) {
-    // sixteen vectors a thread; fewer, down to two, where that leaves an SM less than eight blocks
+    // As few threads a row, 32 at least and 256 at most, as leave a thread four vectors or one round of loads. With 256
+    // for every row 12149 x 2123 bf16 take 63 us instead of 32, 20000 x 1000 63 instead of 18, 64 x 1000 2.1 instead of 2.5;
+    // with one row a block 100000 x 65 fp32 take 105 us instead of 43.
     const int vecs = V / RowVecs<T>::N + 2;
-    int per = 16;
-    while (per > 2 && (long long)rows * ceil_div(vecs, 256 * per) < 8 * ctx.num_sms) per /= 2;
-    const int parts = ceil_div(vecs, 256 * per);
-    launch_pdl(ctx, token_logprobs_bwd_kernel<T>, dim3(rows * parts), dim3(256), 0, logits, ld, V, 1.f / temperature, targets,
-               lse, dlogp, entropy, dentropy, dlogits, ldd, parts, ctx.status);
+    auto launch = [&](auto threads) {
+        constexpr int NT = decltype(threads)::value, ROWS = NT < 128 ? 128 / NT : 1;
+        // sixteen vectors a thread; fewer, down to two, where that leaves an SM less than eight blocks
+        int per = 16;
+        while (per > 2 && (long long)rows * ceil_div(vecs, NT * per) < 8 * ctx.num_sms) per /= 2;
+        const int parts = ceil_div(vecs, NT * per);
+        launch_pdl(ctx, token_logprobs_bwd_kernel<T, NT>, dim3(ceil_div(rows, ROWS) * parts), dim3(NT * ROWS), 0, logits, ld,
+                   rows, V, 1.f / temperature, targets, lse, dlogp, entropy, dentropy, dlogits, ldd, parts, ctx.status);
+    };
+    if (vecs <= 32 * 4) launch(std::integral_constant<int, 32>());
+    else if (vecs <= 64 * 4) launch(std::integral_constant<int, 64>());
+    else if (vecs <= 128 * 4) launch(std::integral_constant<int, 128>());
+    else launch(std::integral_constant<int, 256>());
     ++*ctx.launches;
 }
 

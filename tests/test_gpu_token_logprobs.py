@@ -306,6 +306,15 @@ def test_gradient_of_every_kind_of_row(dtype, V, use):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R", [1, 3, 37, 301, 2501])
+@pytest.mark.parametrize("V", [3, 65, 500, 1005, 2040, 3989])
+def test_gradient_row_counts(dtype, R, V):
+    """Short rows share a block, which the last of them need not fill; few rows are split."""
+    kinds = [KINDS[(i * 5) % len(KINDS)] for i in range(R)]
+    _check_backward(_rows(kinds, V, dtype, R), 1.1, pad=1, seed=R)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("pad,shift", [(0, 0), (1, 0), (3, 1), (8, 5)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_gradient_strides_starts_and_in_place(dtype, pad, shift, in_place):
