@@ -46,7 +46,7 @@ __device__ __forceinline__ f32x2 finish2(int a0, int a1, f32x2 sa, f32x2 sb, f32
 
 // ---------------------------------------------------------------- tensor cores
 // 16384 x 2304 x 768 with bias 31 us (1.9 POP/s; writing the 75 MB result alone takes 22.6 us), 16384 x 768 x 768 with
-// residual 31 us, 2048 x 6400 x 1600 with GELU 26 us, 8192^3 400 us (2.7 POP/s; 330 us with operands of zeros: power).
+// residual 29 us, 2048 x 6400 x 1600 with GELU 26 us, 8192^3 400 us (2.7 POP/s; 330 us with operands of zeros: power).
 //
 // Persistent kernel: a CTA, or a pair of CTAs (a cluster of two, cta_group::2), walks output
 // tiles of 128 CTAS x BN. Warp 0 streams 128-byte-wide K blocks of both operands with TMA into a

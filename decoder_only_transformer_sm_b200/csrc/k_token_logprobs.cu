@@ -13,13 +13,14 @@
 // few long rows the blocks of a cluster). A thread keeps a running (m, s, w) and rescales it
 // when a load of several vectors raises m; the threads join theirs at the end, the blocks
 // through distributed shared memory. Top alternatives come from the same pass: a thread
-// knows its largest value at the end, and the top_k-th largest of those is a bound that
-// at least top_k values of the row reach. Only threads that reach it can hold one of the
-// top_k: what they read is read again (from L2), and the few values that reach the bound
-// are ranked by 64-bit keys (value, then lowest index). Where many values equal the bound, only
-// the larger ones are gathered, and the first equal ones in the row's order after them; the
-// same way -inf fills up where fewer than top_k threads saw a number. (Where even the larger
-// ones are too many, a few threads holding most of a row's largest values, each warp keeps a sorted list.)
+// knows its largest value at the end (of a warp, those of two halves of its vectors), and the
+// top_k-th largest of those is a bound that at least top_k values of the row reach. Only vectors
+// of threads (halves) that reach it can hold one of the top_k: they are read again (from L2), and
+// the few values that reach the bound are ranked by 64-bit keys (value, then lowest index). Where
+// many values equal the bound, only the larger ones are gathered, and the first equal ones in the
+// row's order after them; the same way -inf fills up where fewer than top_k threads saw a number.
+// (Where even the larger ones are too many, a few threads holding most of a row's largest values,
+// each warp keeps a sorted list.)
 // 8192 x 50257 bf16: 135 us without alternatives (6.1 TB/s), 153 with five, 229 with 32.
 #include <cooperative_groups.h>
 
@@ -232,13 +233,19 @@ __device__ __forceinline__ void meet() {
     else __syncthreads();
 }
 
+// A row's vectors are taken by turns into groups, whose largest values bound the k-th largest from
+// below: a thread's vectors, or for a warp (32 values bound too loosely) every other of a thread's.
+template <int NT>
+constexpr int GROUPS_OF = NT < 64 ? 64 : NT;
+
 template <int NT>
 struct ForwardSmem {
-    alignas(16) unsigned largest[NT];     // order of each thread's largest value
-    static constexpr int ROOM = NT < 128 ? 96 : 192;
+    static constexpr int GROUPS = GROUPS_OF<NT>;
+    alignas(16) unsigned largest[GROUPS];   // order of each group's largest value
+    static constexpr int ROOM = NT < 128 ? 256 : 192;   // a warp: 32 vectors of 8, where there are no more
     u64 cand[ROOM];                       // keys that reach the bound (the warps' lists: NT at most)
     Sums sums[NT / 32];
-    int again[NT];                        // the threads whose values are read again
+    int again[GROUPS];                    // the groups whose values are read again
     int scan[NT / 32];
     unsigned bound;
     int n_cand, n_again;
@@ -267,61 +274,61 @@ constexpr int WALK = 8;
 
 constexpr unsigned ORDER_NEG_INF = 0x007fffffu;   // order_of(-inf)
 
-    // Adds to sm.cand the first `need` (at most 32) values of this order among the vectors begin .. end - 1,
+// Adds to sm.cand the first `need` (at most 32) values of this order among the vectors begin .. end - 1,
 // in the order of the row. (Like `lists` a function of its own: rarely needed, and registers.)
-    template <typename T, int NT>
+template <typename T, int NT>
 __device__ __noinline__ void fill(ForwardSmem<NT>& sm, const T* x, const RowVecs<T> rv, int begin, int end, unsigned order,
                                   int need) {
     constexpr int N = RowVecs<T>::N, PER = NT / 32;
-        const int tid = threadIdx.x % NT, lane = tid & 31, n0 = sm.n_cand;
-        const int head = end > rv.full ? rv.head : 0, from = rv.head + min(begin, rv.full) * N - head;
-        const int total = head + max(0, min(end, rv.full) - begin) * N +
-                          (end > rv.full + 1 ? rv.V - (rv.head + rv.full * N) : 0);
-        int found = 0;
-        for (int e0 = 0; e0 < total && found < need; e0 += NT * 8) {
-            unsigned hit = 0;
+    const int tid = threadIdx.x % NT, lane = tid & 31, n0 = sm.n_cand;
+    const int head = end > rv.full ? rv.head : 0, from = rv.head + min(begin, rv.full) * N - head;
+    const int total = head + max(0, min(end, rv.full) - begin) * N +
+                      (end > rv.full + 1 ? rv.V - (rv.head + rv.full * N) : 0);
+    int found = 0;
+    for (int e0 = 0; e0 < total && found < need; e0 += NT * 8) {
+        unsigned hit = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int e = e0 + tid * 8 + j;
-                if (e < total && order_of(to_f(x[e < head ? e : from + e])) == order) hit |= 1u << j;
-            }
-            int before = __popc(hit);   // of this and the lanes before, then of all threads before
-            for (int o = 1; o < 32; o *= 2) {
-                const int v = __shfl_up_sync(0xffffffffu, before, o);
-                if (lane >= o) before += v;
-            }
-            if (lane == 31) sm.scan[tid >> 5] = before;
-            before -= __popc(hit);
-            meet<NT>();
-            int all = 0;
-            for (int w = 0; w < PER; ++w) {
-                if (w < (tid >> 5)) before += sm.scan[w];
-                all += sm.scan[w];
-            }
-            for (int rank = found + before; hit && rank < need; hit &= hit - 1, ++rank) {
-                const int e = e0 + tid * 8 + __ffs(hit) - 1;
-                sm.cand[n0 + rank] = key_of(order, e < head ? e : from + e);
-            }
-            found += all;
-            meet<NT>();
+        for (int j = 0; j < 8; ++j) {
+            const int e = e0 + tid * 8 + j;
+            if (e < total && order_of(to_f(x[e < head ? e : from + e])) == order) hit |= 1u << j;
         }
-        if (tid == 0) sm.n_cand = n0 + min(found, need);
+        int before = __popc(hit);   // of this and the lanes before, then of all threads before
+        for (int o = 1; o < 32; o *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += v;
+        }
+        if (lane == 31) sm.scan[tid >> 5] = before;
+        before -= __popc(hit);
+        meet<NT>();
+        int all = 0;
+        for (int w = 0; w < PER; ++w) {
+            if (w < (tid >> 5)) before += sm.scan[w];
+            all += sm.scan[w];
+        }
+        for (int rank = found + before; hit && rank < need; hit &= hit - 1, ++rank) {
+            const int e = e0 + tid * 8 + __ffs(hit) - 1;
+            sm.cand[n0 + rank] = key_of(order, e < head ? e : from + e);
+        }
+        found += all;
         meet<NT>();
     }
+    if (tid == 0) sm.n_cand = n0 + min(found, need);
+    meet<NT>();
+}
 
-// Leaves in sm.cand the top_k of the chosen threads' values that reach `bound`, of each warp's threads.
+// Leaves in sm.cand the top_k of the chosen groups' values that reach `bound`, of those that each warp reads.
 template <typename T, int NT>
 __device__ __noinline__ void lists(ForwardSmem<NT>& sm, const T* x, const RowVecs<T> rv, int begin, int end, unsigned bound,
                                    int top_k) {
-    constexpr int N = RowVecs<T>::N, PER = NT / 32;
+    constexpr int N = RowVecs<T>::N, PER = NT / 32, GROUPS = GROUPS_OF<NT>;
     const int tid = threadIdx.x % NT, lane = tid & 31, n_again = sm.n_again;
     u64 list = 0;
-    // 32 lanes read a thread's vectors of STEPS steps
+    // 32 lanes read STEPS vectors of a group
     constexpr int STEPS = 32 / N;
     for (int g = tid >> 5; g < n_again; g += PER) {
         const int mine = sm.again[g], j = lane % N;
-        for (int i0 = begin; i0 < end; i0 += STEPS * NT) {
-            const int i = i0 + lane / N * NT + mine;
+        for (int i0 = begin; i0 < end; i0 += STEPS * GROUPS) {
+            const int i = i0 + lane / N * GROUPS + mine;
             const int e = i < end ? rv.first(i) + j : 0;
             const bool is = i < end && e < rv.last(i);
             const unsigned o = is ? order_of(to_f(x[e])) : 0u;
@@ -346,24 +353,25 @@ struct Part {
     const T* x;
     const RowVecs<T>& rv;
     int begin, end;
-    static constexpr int N = RowVecs<T>::N, PER = NT / 32;
+    static constexpr int N = RowVecs<T>::N, GROUPS = GROUPS_OF<NT>, PER = GROUPS / 32;
 
-    // sm.again, sm.n_again: the threads whose largest value reaches `bound` (n_again is 0, all have met).
+    // sm.again, sm.n_again: the groups whose largest value reaches `bound` (n_again is 0, all have met).
     __device__ __forceinline__ void choose(unsigned bound) {
         const int tid = threadIdx.x % NT;
-        if (sm.largest[tid] >= bound) sm.again[atomicAdd(&sm.n_again, 1)] = tid;
+        for (int g = tid; g < GROUPS; g += NT)
+            if (sm.largest[g] >= bound) sm.again[atomicAdd(&sm.n_again, 1)] = g;
         meet<NT>();
     }
-    __device__ __forceinline__ void forget() {   // the candidates and the threads chosen
+    __device__ __forceinline__ void forget() {   // the candidates and the groups chosen
         meet<NT>();
         if (threadIdx.x % NT == 0) sm.n_cand = sm.n_again = 0;
         meet<NT>();
     }
 
-    // Adds the keys of the chosen threads' values that reach `bound` to sm.cand, as far as there is room;
+    // Adds the keys of the chosen groups' values that reach `bound` to sm.cand, as far as there is room;
     // sm.n_cand counts them all.
     __device__ __forceinline__ void gather(unsigned bound, bool any_nan) {
-        const int tid = threadIdx.x % NT, steps = ceil_div(end - begin, NT), n_again = sm.n_again;
+        const int tid = threadIdx.x % NT, steps = ceil_div(end - begin, GROUPS), n_again = sm.n_again;
         const float bound_value = value_of(bound);
         constexpr int R = 2;
         for (int k0 = tid; k0 < n_again * steps; k0 += R * NT) {
@@ -371,8 +379,8 @@ struct Part {
             int at[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int k = k0 + r * NT, g = k / steps;   // vector k % steps of thread again[g]
-                at[r] = g < n_again ? begin + (k - g * steps) * NT + sm.again[g] : end;
+                const int k = k0 + r * NT, g = k / steps;   // vector k % steps of group again[g]
+                at[r] = g < n_again ? begin + (k - g * steps) * GROUPS + sm.again[g] : end;
                 q[r] = at[r] < end ? load_vec(x, rv, at[r], end) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
@@ -401,12 +409,37 @@ struct Part {
     // part's top_k (all of them, if it has fewer values). any_nan: there is NaN or +inf.
     __device__ __forceinline__ void find_top(int top_k, bool any_nan) {
         const int tid = threadIdx.x % NT, lane = tid & 31;
-        if (top_k <= WALK || NT == 32) {
+        if (NT == 32 && top_k > WALK) {   // every lane counts those above its own
+            const unsigned mine[2] = {sm.largest[lane], sm.largest[lane + 32]};
+            int above[2] = {0, 0};
+#pragma unroll 4
+            for (int j = 0; j < GROUPS; j += 4) {
+                const uint4 g = *reinterpret_cast<const uint4*>(sm.largest + j);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    above[i] += (g.x > mine[i]) + (g.y > mine[i]) + (g.z > mine[i]) + (g.w > mine[i]);
+            }
+            unsigned least = 0xffffffffu;
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool is = above[i] < top_k && mine[i] > ORDER_NEG_INF;
+                const unsigned in = __ballot_sync(0xffffffffu, is);
+                if (is) sm.again[n + __popc(in & ((1u << lane) - 1))] = lane + 32 * i;
+                if (is) least = min(least, mine[i]);
+                n += __popc(in);
+            }
+            least = __reduce_min_sync(0xffffffffu, least);
+            if (lane == 0) {
+                sm.bound = least;
+                sm.n_again = n;
+            }
+        } else if (top_k <= WALK) {
             if (tid < 32) {
                 unsigned key[PER], bound = 0xffffffffu;
 #pragma unroll
                 for (int i = 0; i < PER; ++i) key[i] = sm.largest[lane + 32 * i];
-                // distinct values from the largest on, until top_k threads have reached them
+                // distinct values from the largest on, until top_k groups have reached them
                 for (int n = 0; n < top_k && bound > ORDER_NEG_INF;) {
                     unsigned below = 0;
 #pragma unroll
@@ -443,9 +476,9 @@ struct Part {
         }
         meet<NT>();
         const int n_again = sm.n_again;
-        const bool few = n_again < top_k;   // threads that saw a number: all their numbers count
+        const bool few = n_again < top_k;   // groups with a number: all their numbers count
         const unsigned bound = few ? ORDER_NEG_INF + 1 : sm.bound;
-        bool fits = n_again <= 2 * top_k || n_again * ceil_div(end - begin, NT) * N <= sm.ROOM;
+        bool fits = n_again <= 2 * top_k || n_again * ceil_div(end - begin, GROUPS) * N <= sm.ROOM;
         if (fits) {
             gather(bound, any_nan);
             fits = sm.n_cand <= sm.ROOM;
@@ -478,7 +511,7 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
                                                                       int rows, int V, float inv_tau,
                                                                       const int* __restrict__ targets, LogprobOut out,
                                                                       int parts, unsigned* status) {
-    constexpr int U = 4, ROWS = BLOCK_OF<NT> / NT;
+    constexpr int U = 4, ROWS = BLOCK_OF<NT> / NT, H = GROUPS_OF<NT> / NT;   // H groups a thread
     __shared__ ForwardSmem<NT> sms[ROWS];
     ForwardSmem<NT>& sm = sms[threadIdx.x / NT];
     const int tid = threadIdx.x % NT, lane = tid & 31;
@@ -498,7 +531,25 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
     }
 
     Sums a = {LOWEST, 0.f, 0.f};
-    float largest = NEG_INF;
+    float largest[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) largest[h] = NEG_INF;
+    // q's extremes; vector u is of the group u % H
+    auto look = [&](const uint4 (&q)[U], float& top, float& low) {
+        top = NEG_INF;
+        low = -NEG_INF;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            uint4 some[U / H];
+#pragma unroll
+            for (int u = 0; u < U / H; ++u) some[u] = q[u * H + h];
+            float t, l;
+            extremes(some, t, l, T());
+            largest[h] = fmaxf(largest[h], t);
+            top = fmaxf(top, t);
+            low = fminf(low, l);
+        }
+    };
     {
         // batches of U whole vectors
         int i = begin + tid;
@@ -509,8 +560,7 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
 #pragma unroll
             for (int u = 0; u < U; ++u) q[u] = __ldg(at + i + u * NT);
             float top, low;
-            extremes(q, top, low, T());
-            largest = fmaxf(largest, top);
+            look(q, top, low);
             if (top > a.m) a.raise(top, c);
             if (low > -1e30f) a.add<false, T>(q, c);
             else a.add<true, T>(q, c);
@@ -520,20 +570,23 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
 #pragma unroll
             for (int u = 0; u < U; ++u) q[u] = load_vec(x, rv, i + u * NT, end);
             float top, low;
-            extremes(q, top, low, T());
-            largest = fmaxf(largest, top);
+            look(q, top, low);
             if (top > a.m) a.raise(top, c);
             a.add<true, T>(q, c);
         }
     }
 
     if (out.top_k) {
-        unsigned order = begin + tid < end ? order_of(largest) : 0u;
-        if (a.s != a.s) {   // a NaN, or +inf: find out which
-            for (int i = begin + tid; i < end; i += NT)
-                for (int v = rv.first(i); v < rv.last(i); ++v) order = max(order, order_of(to_f(x[v])));
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const int g = tid + h * NT;
+            unsigned order = begin + g < end ? order_of(largest[h]) : 0u;
+            if (a.s != a.s) {   // a NaN, or +inf: find out which
+                for (int i = begin + g; i < end; i += GROUPS_OF<NT>)
+                    for (int v = rv.first(i); v < rv.last(i); ++v) order = max(order, order_of(to_f(x[v])));
+            }
+            sm.largest[g] = order;
         }
-        sm.largest[tid] = order;
     }
     // the maximum of all first, so that every thread rescales once
     {
@@ -725,9 +778,11 @@ void launch_token_logprobs(const Ctx& ctx, const T* logits, long long ld, int ro
                            const int* targets, const LogprobOut& out) {
     const float inv_tau = 1.f / temperature;
     // A warp a row where the row is short, and with many rows up to 8192: no block to wait for (8192 rows of 1024 bf16
-    // logits 11.8 us against 22, of 8192 with five alternatives 40.7 against 50.8). Not for many alternatives: the
-    // bound of 32 threads' values is too loose for them.
-    const bool warp = out.top_k <= WALK && (V <= 2048 || (V <= 8192 && rows >= 8 * ctx.num_sms));
+    // logits 11.8 us against 22, of 8192 with five alternatives 40.7 against 50.8). For many alternatives, which a warp
+    // takes longer to rank, only with many rows, of up to 16 KB (with 20: 20000 x 512 bf16 38 us against 92, 8192 x
+    // 8192 53 against 65; but 8192 x 6000 fp32 61 against 56, 200 x 1500 6.6 against 4.9).
+    const bool many = rows >= 8 * ctx.num_sms;
+    const bool warp = out.top_k <= WALK ? V <= 2048 || (V <= 8192 && many) : many && V <= 16384 / (int)sizeof(T);
     // Few rows: as many blocks a row as give every SM two, while a thread still has a vector.
     int parts = 8;
     while (parts > 1 && ((long long)rows * parts > 2 * ctx.num_sms || V < parts * 128 * RowVecs<T>::N)) parts /= 2;

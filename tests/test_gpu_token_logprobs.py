@@ -188,6 +188,15 @@ def test_row_counts(dtype, R, V):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [33, 65, 200, 300, 511, 700, 1021, 2049, 4096])
+@pytest.mark.parametrize("k", [9, 20, 32])
+def test_many_short_rows_with_many_alternatives(dtype, V, k):
+    """1203 rows: a warp takes a whole one, the last block has three."""
+    kinds = [KINDS[(i * 5) % len(KINDS)] for i in range(1203)]
+    _check_forward(_rows(kinds, V, dtype, V + k), 0.9, k, pad=V % 3, seed=V)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("tau", [0.05, 0.7, 1.0, 3.0])
 @pytest.mark.parametrize("pad,shift", [(0, 0), (1, 0), (3, 1), (8, 5), (64, 8)])
 def test_temperatures_strides_and_starts(dtype, tau, pad, shift):
