@@ -242,8 +242,10 @@ template <int NT>
 struct ForwardSmem {
     static constexpr int GROUPS = GROUPS_OF<NT>;
     alignas(16) unsigned largest[GROUPS];   // order of each group's largest value
-    static constexpr int ROOM = NT < 128 ? 256 : 192;   // a warp: 32 vectors of 8, where there are no more
-    u64 cand[ROOM];                       // keys that reach the bound (the warps' lists: NT at most)
+    // 256: what a warp finds in 32 vectors of 8, or the lists of eight. 192 hold the lists of four.
+    static constexpr int ROOM = NT == 128 ? 192 : 256;
+    static_assert(ROOM >= NT / 32 * LOGPROB_MAX_TOP, "each warp's list fits");
+    u64 cand[ROOM];                       // keys that reach the bound
     Sums sums[NT / 32];
     int again[GROUPS];                    // the groups whose values are read again
     int scan[NT / 32];

@@ -552,3 +552,36 @@ def test_calls_at_once_on_two_streams():
     for w, r in zip(works, want):
         assert int(w.status.item()) == 0
         assert all(torch.equal(a, b) for a, b in zip(w.results(), r))
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 32768), (torch.float32, 50257), (torch.bfloat16, 65536),
+                                     (torch.bfloat16, 70001)])
+@pytest.mark.parametrize("k", [9, 24, 25, 32])
+def test_largest_values_of_many_long_rows_with_few_threads(dtype, V, k):
+    """Rows of 120 KB and more, a block of 256 threads each (more rows than SMs): each warp's list of alternatives has
+    room, where the allowed, or just the largest, values lie side by side or all with a few of the threads."""
+    from decoder_only_transformer_sm_b200 import native
+    N = 16 // torch.tensor([], dtype=dtype).element_size()      # of a vector; vectors go to the 256 threads in turn
+    rng = np.random.default_rng(V + k)
+    i = np.arange(V)
+    chosen = [(i >= 1000) & (i < 1240), (i >= V - 700) & (i < V - 400)]
+    chosen += [i // N % 256 < n for n in (1, 8, k - 1, k, 40)] + [(i // N % 256 % 8 == 3) & (i // N % 256 < 8 * (k - 1))]
+    kinds = []
+    for c in chosen:
+        noise = rng.standard_normal(V)
+        kinds += [np.where(c, noise, -np.inf), np.where(c, 6.0 + noise, 0.1 * noise)]
+    x = torch.from_numpy(np.stack(kinds).astype(np.float32)).to(dtype)
+    R = len(kinds) * 11                                         # 176 rows: not split
+    o = _oracle(x, 1.0, np.zeros(len(kinds), np.int64), k)
+    ids, top = torch.empty((R, k), dtype=torch.int32, device="cuda"), torch.empty((R, k), device="cuda")
+    lse = torch.empty(R, device="cuda")
+    _, dx = _place(x.repeat(11, 1), -V % 8, 0)
+    native.token_logprobs(dx, V, 1.0, lse=lse, top_ids=ids, top_logp=top)
+    np.testing.assert_array_equal(ids.cpu().numpy(), np.tile(o["ids"], (11, 1)))
+    # 256 threads: V / 512 additions of a pair's sum, 5 + 8 joins
+    Z = np.tile(_spread(o), 11)
+    tol = 6 * EPS * Z + 2.0 ** -21 + (V / 512 + 16) * EPS
+    _close(lse.cpu().numpy(), np.tile(o["lse"], 11), tol + 3 * EPS * (np.abs(np.tile(o["lse"], 11)) + Z), "lse")
+    want = np.tile(o["top"], (11, 1))
+    size = np.where(np.isfinite(want), np.abs(want), 0.0)
+    _close(top.cpu().numpy(), want, tol[:, None] + 6 * EPS * (2 * size + Z[:, None]), "top_logp")
