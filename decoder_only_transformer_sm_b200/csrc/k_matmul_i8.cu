@@ -363,6 +363,15 @@ __global__ void __launch_bounds__(Tile<BN, CTAS, BYTES>::THREADS, 1)
                     }
                 }
             }
+            if (PAIR && rank == 1) {
+                // The first CTA's MMAs also arrive here: its shared memory must outlive the last of these arrivals, those
+                // that free the last stages and `drain` (acc_full's are the epilogue's). Waited for after the last load,
+                // so that the limit is on the last K blocks, not on the whole product.
+                volatile uint32_t no_abort = 0;
+                for (uint32_t j = it > L::STAGES ? it - L::STAGES : 0; j < it && ok; ++j)
+                    ok = tc::mbar_wait(&ctl->empty[j % L::STAGES], (j / L::STAGES) & 1, abort, status);
+                tc::mbar_wait(&ctl->drain, 0, &no_abort, status);
+            }
         }
     } else if (warp == 1 || warp == LAST) {
         if (lane == 0 && rank == 0) {

@@ -304,3 +304,22 @@ def test_quantised_linear_layer_on_a_side_stream_and_in_a_graph():
     half = (xs[0].double().abs().amax(1, keepdim=True) / 254)
     bound = half * w.double().abs().sum(1) + (ws.double() / 2) * (xs[0].double().abs().sum(1, keepdim=True) + K * half)
     assert torch.all((want[0].double() - ref).abs() <= 1.13 * bound + 2.0 ** -7 * ref.abs() + 1e-4)
+
+
+def test_pairs_of_blocks_one_product_after_another():
+    """Products on pairs of blocks (256 x 256 tiles), each with the next one's blocks waiting for its SMs: a block of a
+    pair stays until the other's last arrivals on its barriers. One K block, and more than the ring has stages."""
+    from decoder_only_transformer_sm_b200 import native
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for M, N, K in ((4096, 8192, 64), (4096, 4864, 784)):
+        a = torch.randint(-127, 128, (M, K), generator=g, dtype=torch.int8, device="cuda")
+        b = torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int8, device="cuda")
+        sa, sb = torch.rand(M, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda")
+        outs = [torch.empty((M, N), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        for i in range(40):
+            native.matmul_i8(a, sa, b, sb, outs[i % 4], status=status)
+        assert int(status.item()) == 0
+        want = (a.double() @ b.double().t()) * sa.double()[:, None] * sb.double()
+        for out in outs:   # three roundings of fp32, one of bf16
+            assert torch.all((out.double() - want).abs() <= (2.0 ** -8 * 1.01 + 4 * 2.0 ** -24) * want.abs())
