@@ -258,6 +258,8 @@ extern "C" int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scal
         if (!resid) return set_error(GPT2_ERR_INVALID_ARG, "epilogue operand missing");
         if (out_dtype != GPT2K_F32) return set_error(GPT2_ERR_INVALID_ARG, "bias_resid writes fp32");
         if (ldr < N) return set_error(GPT2_ERR_INVALID_ARG, "need ldr >= N");
+        if (resid == out && ldr != ldo && M > 1)
+            return set_error(GPT2_ERR_INVALID_ARG, "a result in place of the residual has its row stride");
     }
     if (misaligned(a_scale, 4) || misaligned(b_scale, 4) || misaligned(out, elem_size(out_dtype)) ||
         misaligned(bias, 4) || misaligned(resid, 4) || misaligned(status_dev, 4))

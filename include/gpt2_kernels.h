@@ -201,14 +201,15 @@ int gpt2k_quantize_rows(int dtype, const void* x, int rows, int K, int64_t ldx, 
  *   GPT2K_EPI_BIAS       out = u + bias[n]
  *   GPT2K_EPI_BIAS_GELU  out = gelu_tanh(u + bias[n])   (no derivative output)
  *   GPT2K_EPI_BIAS_RESID out = resid[m][n] + u + bias[n]   (GPT2K_F32 only;
- *                        resid fp32, row stride ldr; it may be out itself)
+ *                        resid fp32, row stride ldr; it may be out itself,
+ *                        with ldr = ldo, but not overlap it otherwise)
  * out has row stride ldo elements; columns N .. ldo - 1 are left as they are.
  * out must not overlap A or B. Operands may start anywhere an element may:
  * A and B whose first byte and row stride are multiples of 16 are loaded by
  * TMA or, for a few rows, streamed; other ones are put together from bytes
  * (slower). Errors: INVALID_ARG (sizes < 1, M or N above 2^30, K > 131071, a
  * stride below its row, another epilogue, an operand of the epilogue missing, bias_resid with a bf16
- * result, a NULL or misaligned pointer). */
+ * result or in place with another stride, a NULL or misaligned pointer). */
 int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B, int64_t ldb,
                     const float* b_scale, int M, int N, int K, int epilogue, int out_dtype, void* out, int64_t ldo,
                     const float* bias, const float* resid, int64_t ldr, uint32_t* status_dev, void* stream);

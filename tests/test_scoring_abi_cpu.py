@@ -111,3 +111,19 @@ def test_fp32_quotient_is_within_its_bound():
         for y in (np.nextafter(odd, np.float32(np.inf)), np.nextafter(odd, np.float32(-np.inf))):
             off = 2 * 127.0 * y.astype(np.float64) / float(a)
             assert np.all(off != np.rint(off))
+
+
+def test_residual_in_place_with_another_stride_is_refused():
+    """A tile's results would overwrite residuals that other tiles still read."""
+    lib = native.load_library()
+    #      0  1   2  3  4   5  6  7  8   9  10 11 12 13 14 15 16 17
+    ok = (P, 16, P, P, 16, P, 4, 8, 16, 3, 0, P, 8, P, P, 8, ODD, None)   # (all but the status word, checked last)
+    assert lib.gpt2k_matmul_i8(*ok) == -1 and b"aligned" in lib.gpt2_last_error()
+    for ldo, ldr in ((8, 9), (16, 8)):
+        args = list(ok)
+        args[12], args[15] = ldo, ldr
+        assert lib.gpt2k_matmul_i8(*args) == -1 and b"in place" in lib.gpt2_last_error()
+    # one row has no stride
+    args = list(ok)
+    args[6], args[15] = 1, 9
+    assert lib.gpt2k_matmul_i8(*args) == -1 and b"aligned" in lib.gpt2_last_error()
