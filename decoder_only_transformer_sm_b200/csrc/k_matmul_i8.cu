@@ -651,8 +651,13 @@ bool launch_kind(const Ctx& ctx, const I8Product& p, bool whole) {
 
 }  // namespace
 
-bool launch_matmul_i8(const Ctx& ctx, const I8Product& p) {
+bool launch_matmul_i8(const Ctx& ctx, const I8Product& product) {
     ++*ctx.launches;
+    // A single row's stride is never used, so it must not decide the path: one token of K bytes, packed, would send
+    // padded weights through the rows that start anywhere (1 x 50304 x 763: 41 us, 20 as whole segments).
+    I8Product p = product;
+    if (p.M == 1) p.lda = (p.K + 15) / 16 * 16;
+    if (p.N == 1) p.ldb = (p.K + 15) / 16 * 16;
     const bool whole = whole_segments(p.A, p.lda, 1) && whole_segments(p.B, p.ldb, 1), f32 = p.out_f32;
     if (p.M <= I8_FEW_ROWS) {
         launch_matmul_i8_rows(ctx, p, whole);

@@ -280,7 +280,8 @@ __global__ void __launch_bounds__(QT, 1024 / QT) quantize_rows_kernel(const T* _
 template <typename T, int G, int QT = (G > 128 ? G : 128)>
 void launch_short(const Ctx& ctx, const T* x, long long ldx, int rows, int K, int8_t* q, long long ldq, float* scale) {
     constexpr int N = 16 / sizeof(T);
-    const bool aligned = ((uintptr_t)x & 15) == 0 && ((uintptr_t)q & (N - 1)) == 0 && (ldx | ldq | K) % N == 0;
+    const long long strides = rows > 1 ? ldx | ldq : 0;   // one row has none (1 x 6400 bf16: 2.7 us as unaligned, 2.0)
+    const bool aligned = ((uintptr_t)x & 15) == 0 && ((uintptr_t)q & (N - 1)) == 0 && (strides | K) % N == 0;
     const int grid = ceil_div(rows, QT / G);
     if (aligned)
         launch_pdl(ctx, quantize_rows_kernel<T, G, QT, true>, dim3(grid), dim3(QT), 0, x, ldx, rows, K, q, ldq, scale);

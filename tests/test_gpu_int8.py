@@ -323,3 +323,60 @@ def test_pairs_of_blocks_one_product_after_another():
         want = (a.double() @ b.double().t()) * sa.double()[:, None] * sb.double()
         for out in outs:   # three roundings of fp32, one of bf16
             assert torch.all((out.double() - want).abs() <= (2.0 ** -8 * 1.01 + 4 * 2.0 ** -24) * want.abs())
+
+
+def _replay_time(call):
+    """Shortest of twelve replays of a graph of ten calls, in us a call."""
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(10):
+            call()
+    best = float("inf")
+    for _ in range(12):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 100.0)
+    return best
+
+
+def test_stride_of_a_single_row_does_not_matter():
+    """One token's packed codes beside padded weights, and one output channel beside padded tokens: right, and no slower
+    than the same operands with a padded row (20 us; the path of rows that start anywhere takes 41)."""
+    from decoder_only_transformer_sm_b200 import native
+    g = torch.Generator(device="cuda").manual_seed(2)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    K = 763
+
+    def operand(rows, pad):
+        hold = torch.randint(-127, 128, (rows, K + pad), generator=g, dtype=torch.int8, device="cuda")
+        return hold[:, :K]
+
+    for M, N, dtype in ((1, 50304, torch.bfloat16), (1, 100, torch.float32), (300, 1, torch.float32), (5, 1, torch.bfloat16),
+                        (1, 1, torch.float32)):
+        a, b = operand(M, 5), operand(N, 5)
+        sa, sb = torch.rand(M, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda")
+        want = (a.double() @ b.double().t()) * sa.double()[:, None] * sb.double()
+        tol = (4 * 2.0 ** -24 + (2.0 ** -8 * 1.01 if dtype == torch.bfloat16 else 0.0)) * want.abs()
+        times = []
+        for pa, pb in ((a, b), (a.contiguous() if M == 1 else a, b.contiguous() if N == 1 else b),
+                       (operand(1, 8).copy_(a) if M == 1 else a, operand(1, 8).copy_(b) if N == 1 else b)):
+            out = torch.empty((M, N), dtype=dtype, device="cuda")
+            native.matmul_i8(pa, sa, pb, sb, out, status=status)
+            assert torch.all((out.double() - want).abs() <= tol)
+            if N > 10000:
+                times.append(_replay_time(lambda: native.matmul_i8(pa, sa, pb, sb, out, status=status)))
+        assert not times or max(times) <= 1.4 * times[0], times
+    for K_, dtype in ((6400, torch.bfloat16), (8192, torch.float32), (40, torch.bfloat16)):
+        x = torch.randn((1, K_ + 3), generator=g, device="cuda").to(dtype)[:, :K_]
+        room = torch.full((1, K_ + 5), 77, dtype=torch.int8, device="cuda")
+        scale = torch.empty(1, device="cuda")
+        native.quantize_rows(x, room[:, :K_], scale)
+        want_q, want_s = _codes64(x.float().cpu().numpy())
+        np.testing.assert_array_equal(room[:, :K_].cpu().numpy(), want_q)
+        np.testing.assert_array_equal(scale.cpu().numpy(), want_s)
+        assert torch.all(room[:, K_:] == 77)
