@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
             out.logp[row] = t < 0 ? 0.f : logp_of(to_f(x[t]));
         }
     }
-    if (a.s == 0.f && tid < out.top_k) {   // every logit is -inf
+    if (a.s == 0.f && tid < out.top_k) {   // every logit is -inf (logits whose z all overflow keep their order)
         out.top_ids[(long long)row * out.top_k + tid] = tid;
         out.top_logp[(long long)row * out.top_k + tid] = NEG_INF;
     }

@@ -228,9 +228,10 @@ int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scale, const in
  * NULL; top_k = 0 and NULL top_ids and top_logp for no alternatives, else
  * 1 <= top_k <= min(32, V). At least one output. fp32 arithmetic.
  * A row of which nothing is left (every z = -inf): lse and log probabilities
- * -inf, entropy 0, ids 0 .. top_k - 1. A row with a NaN or z = +inf: NaN in
- * lse, entropy, top_logp and a given target's logp; its ids are ordered with
- * NaN above every number. A target outside [-1, V) sets status bit 0 and is
+ * -inf, entropy 0. A row with a NaN or z = +inf: NaN in lse, entropy, top_logp
+ * and a given target's logp. The ids are those of the logits in both cases too,
+ * with NaN above every number: 0 .. top_k - 1 where every logit is -inf, by
+ * value where finite logits / temperature pass fp32's range. A target outside [-1, V) sets status bit 0 and is
  * clamped into [0, V). Errors: INVALID_ARG (unknown dtype, rows or V < 1,
  * V > 2^30 or rows * (V / 2048 + 1) > 2^30, ld < V, a temperature that is not finite and > 0 or below 4.5e-39 (1.5 /
  * temperature infinite), arguments that do not go together, a NULL or misaligned pointer). */

@@ -585,3 +585,19 @@ def test_largest_values_of_many_long_rows_with_few_threads(dtype, V, k):
     want = np.tile(o["top"], (11, 1))
     size = np.where(np.isfinite(want), np.abs(want), 0.0)
     _close(top.cpu().numpy(), want, tol[:, None] + 6 * EPS * (2 * size + Z[:, None]), "top_logp")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,V", [(5, 40), (5, 3000), (5, 50257), (160, 5003), (160, 70001)])
+def test_rows_whose_scaled_logits_all_overflow(dtype, R, V):
+    """Finite logits below -1.8e38 at temperature 0.5: every z is -inf, so nothing is left of the row; the alternatives
+    are still the largest logits, -inf after them."""
+    rng = np.random.default_rng(V)
+    x = rng.uniform(-3.3e38, -1.8e38, (5, V)).astype(np.float32)
+    x[1] = -2e38
+    x[2, ::2] = -np.inf
+    x[3, 2:] = -np.inf
+    x[4] = np.finfo(np.float32).min if dtype == torch.float32 else -3e38
+    o, _, _ = _check_forward(torch.from_numpy(np.tile(x, (R // 5, 1))).to(dtype), 0.5, 9, pad=-V % 8, seed=R)
+    assert np.all(o["lse"] == -np.inf) and list(o["ids"][3][:2]) in ([0, 1], [1, 0])
+    _check_backward(torch.from_numpy(x).to(dtype), 0.5, pad=-V % 8)
