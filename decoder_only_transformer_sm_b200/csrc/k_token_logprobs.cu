@@ -169,7 +169,7 @@ struct Sums {
     float m, s, w;   // m = -FLT_MAX and s = 0 where nothing was seen
     __device__ __forceinline__ void raise(float to, float c) {
         const float r = ex2_approx((m - to) * c);
-        w = (w - fminf(to - m, 1e30f) * s) * r;   // s is 0 or the difference finite enough
+        w = (w - fminf(to - m, 1e30f) * s) * r;   // cut off only where r is 0 (LOGPROB_MAX_TEMPERATURE) or s is
         s *= r;
         m = to;
     }

@@ -299,8 +299,8 @@ int check_logprob_args(int dtype, const void* logits, int rows, int V, int64_t l
     if (dtype != GPT2K_F32 && dtype != GPT2K_BF16) return set_error(GPT2_ERR_INVALID_ARG, "unknown dtype");
     if (rows < 1 || V < 1 || ld < V) return set_error(GPT2_ERR_INVALID_ARG, "need rows, V >= 1 and ld >= V");
     if (!logits || !status) return set_error(GPT2_ERR_INVALID_ARG, "NULL operand");
-    if (!(temperature > 0.f) || !(temperature < INFINITY) || !(1.5f / temperature < INFINITY))
-        return set_error(GPT2_ERR_INVALID_ARG, "temperature must be finite and > 0, 1.5 / temperature finite");
+    if (!(temperature > 0.f) || !(temperature <= LOGPROB_MAX_TEMPERATURE) || !(1.5f / temperature < INFINITY))
+        return set_error(GPT2_ERR_INVALID_ARG, "temperature must be > 0 and at most 1e20, 1.5 / temperature finite");
     if (V > MAX_EXTENT || (long long)rows * (V / 2048 + 1) > MAX_EXTENT)
         return set_error(GPT2_ERR_INVALID_ARG, "V above 2^30, or rows x V more than one launch takes");
     if (misaligned(logits, elem_size(dtype)) || misaligned(status, 4))

@@ -347,6 +347,9 @@ struct LogprobOut {
     int top_k;
 };
 constexpr int LOGPROB_MAX_TOP = 32;
+// Up to here two logits further apart than 1e30 (or than fp32's range) have a ratio of probabilities of 0, so that
+// the running sums may cut their difference off (k_token_logprobs.cu).
+constexpr float LOGPROB_MAX_TEMPERATURE = 1e20f;
 template <typename T>
 void launch_token_logprobs(const Ctx& ctx, const T* logits, long long ld, int rows, int V, float temperature,
                            const int* targets, const LogprobOut& out);

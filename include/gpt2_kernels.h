@@ -231,10 +231,12 @@ int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scale, const in
  * -inf, entropy 0. A row with a NaN or z = +inf: NaN in lse, entropy, top_logp
  * and a given target's logp. The ids are those of the logits in both cases too,
  * with NaN above every number: 0 .. top_k - 1 where every logit is -inf, by
- * value where finite logits / temperature pass fp32's range. A target outside [-1, V) sets status bit 0 and is
- * clamped into [0, V). Errors: INVALID_ARG (unknown dtype, rows or V < 1,
- * V > 2^30 or rows * (V / 2048 + 1) > 2^30, ld < V, a temperature that is not finite and > 0 or below 4.5e-39 (1.5 /
- * temperature infinite), arguments that do not go together, a NULL or misaligned pointer). */
+ * value where finite logits / temperature pass fp32's range. A target outside
+ * [-1, V) sets status bit 0 and is clamped into [0, V). Errors: INVALID_ARG
+ * (unknown dtype, rows or V < 1, V > 2^30 or rows * (V / 2048 + 1) > 2^30,
+ * ld < V, a temperature that is not > 0, below 4.5e-39 (1.5 / temperature
+ * infinite) or above 1e20 (differences of logits would leave the sums' range),
+ * arguments that do not go together, a NULL or misaligned pointer). */
 int gpt2k_token_logprobs(int dtype, const void* logits, int rows, int V, int64_t ld, float temperature,
                          const int32_t* targets, int top_k, float* logp, float* entropy, float* lse,
                          int32_t* top_ids, float* top_logp, uint32_t* status_dev, void* stream);

@@ -601,3 +601,21 @@ def test_rows_whose_scaled_logits_all_overflow(dtype, R, V):
     o, _, _ = _check_forward(torch.from_numpy(np.tile(x, (R // 5, 1))).to(dtype), 0.5, 9, pad=-V % 8, seed=R)
     assert np.all(o["lse"] == -np.inf) and list(o["ids"][3][:2]) in ([0, 1], [1, 0])
     _check_backward(torch.from_numpy(x).to(dtype), 0.5, pad=-V % 8)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tau", [1e-30, 1e-4, 1e6, 1e20])
+@pytest.mark.parametrize("R,V", [(16, 300), (16, 9000), (160, 5003), (160, 70001)])
+def test_temperatures_of_every_size(dtype, tau, R, V):
+    """Logits of the temperature's size, with the type's lowest values and (last row) differences that fp32 does not
+    hold among them."""
+    kinds = KINDS * (R // len(KINDS)) if V < 60000 else KINDS[:8] * (R // 8)
+    x = _rows(kinds, V, torch.float32, R)
+    low = torch.tensor(torch.finfo(dtype).min, dtype=torch.float32)
+    x = torch.where(x <= -3e38, torch.where(x.isinf(), x, low), x * tau)
+    if V == 300:
+        _check_backward(x.to(dtype), tau, pad=-V % 8, seed=V)
+    x[-1, 0], x[-1, 1], x[-1, 2] = -1e32, -low, low
+    if tau < 1:
+        x[-1, 1] = 1e32 * tau                               # (the largest over tau would be infinite)
+    _check_forward(x.to(dtype), tau, 6, pad=-V % 8, seed=V)

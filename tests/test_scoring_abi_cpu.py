@@ -127,3 +127,16 @@ def test_residual_in_place_with_another_stride_is_refused():
     args = list(ok)
     args[6], args[15] = 1, 9
     assert lib.gpt2k_matmul_i8(*args) == -1 and b"aligned" in lib.gpt2_last_error()
+
+
+def test_temperatures_past_the_limit_are_refused():
+    """Above 1e20 differences of logits no longer fit where the running sums need them (logits of -1e32 and 1e32 at
+    temperature 1e32 lost a part of the entropy)."""
+    lib = native.load_library()
+    fwd = (1, P, 3, 40, 40, 1.0, P, 5, P, P, P, P, ODD, P, None)     # (all but one pointer, checked last)
+    bwd = (1, P, 3, 40, 48, 1.0, P, P, P, P, P, ctypes.c_void_p(4097), 48, P, None)
+    for fn, ok in ((lib.gpt2k_token_logprobs, fwd), (lib.gpt2k_token_logprobs_bwd, bwd)):
+        for tau, said in ((1e20, b"aligned"), (1.0001e20, b"temperature"), (1e32, b"temperature"), (3e38, b"temperature")):
+            args = list(ok)
+            args[5] = tau
+            assert fn(*args) == -1 and said in lib.gpt2_last_error(), (tau, lib.gpt2_last_error())
