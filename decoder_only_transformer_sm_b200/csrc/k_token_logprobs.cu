@@ -645,7 +645,10 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
     const bool bad = a.s != a.s || z_max == -NEG_INF, empty = !bad && (a.s == 0.f || z_max == NEG_INF);
     const float log_s = logf(a.s);
     auto settle = [&](float v, float nothing) { return bad ? nan_value() : empty ? nothing : v; };
-    auto logp_of = [&](float v) { return settle((v - a.m) * inv_tau - log_s, NEG_INF); };
+    auto logp_of = [&](float v) {   // (the difference of two logits may pass fp32's range where that of their z does not)
+        const float d = v - a.m;
+        return settle((d >= LOWEST ? d * inv_tau : v * inv_tau - z_max) - log_s, NEG_INF);
+    };
     if (tid == 0) {
         if (out.lse) out.lse[row] = settle(z_max + log_s, NEG_INF);
         if (out.entropy) out.entropy[row] = settle(log_s - a.w / a.s * inv_tau, 0.f);

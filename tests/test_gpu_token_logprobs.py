@@ -619,3 +619,28 @@ def test_temperatures_of_every_size(dtype, tau, R, V):
     if tau < 1:
         x[-1, 1] = 1e32 * tau                               # (the largest over tau would be infinite)
     _check_forward(x.to(dtype), tau, 6, pad=-V % 8, seed=V)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,V", [(3, 40), (3, 40000), (160, 5003), (160, 70001)])
+def test_a_token_further_below_the_largest_than_fp32_reaches(dtype, R, V):
+    """A forbidden token at the type's lowest value beside a largest one near its largest: their difference is no fp32
+    number, divided by the temperature it is."""
+    from decoder_only_transformer_sm_b200 import native
+    high, low = float(torch.finfo(dtype).max), float(torch.finfo(dtype).min)
+    x = torch.full((R, V), low, dtype=dtype)
+    x[:, 7] = high
+    x[:, 20:] = float("-inf")
+    t = torch.full((R,), 3, dtype=torch.int32, device="cuda")
+    for tau in (1.0, 3.0, 1e6, 1e20):
+        logp, H, lse = (torch.empty(R, device="cuda") for _ in range(3))
+        ids, top = torch.empty((R, 22), dtype=torch.int32, device="cuda"), torch.empty((R, 22), device="cuda")
+        native.token_logprobs(x.cuda(), V, tau, targets=t, logp=logp, entropy=H, lse=lse, top_ids=ids, top_logp=top)
+        gap = _in_fp32_range(np.float64((low - high) / tau))
+        want = np.full((R, 22), -np.inf)
+        want[:, 0], want[:, 1:20] = 0.0, gap
+        size = np.where(np.isfinite(want), np.abs(want), 0.0)
+        _close(top.cpu().numpy(), want, 6 * EPS * size, "top_logp")
+        _close(logp.cpu().numpy(), np.full(R, gap), 6 * EPS * size[0, 1], "logp")
+        _close(lse.cpu().numpy(), np.full(R, high / tau), 6 * EPS * high / tau, "lse")
+        assert torch.all(H == 0) and ids[0].tolist() == [7] + [v for v in range(20) if v != 7] + [20, 21]
