@@ -478,13 +478,21 @@ def _import_torch():
     return torch
 
 
-def _rows_of(t, name, codes, rows=None, cols=None):
-    """(rows, columns, address, row stride, type code) of a 2-D tensor with unit stride inside its rows."""
+# Rows, columns, V and top_k go to the library as 32-bit integers, to which ctypes cuts them off without a word (the
+# library refuses those above 2^30).
+_MAX_INT = (1 << 31) - 1
+
+
+def _rows_of(t, name, codes, rows=None, cols=None, wide=False):
+    """(rows, columns, address, row stride, type code) of a 2-D tensor with unit stride inside its rows; wide: its
+    number of columns is not passed on."""
     code = codes.get(t.dtype)
     if code is None or t.dim() != 2:
         raise ValueError(f"{name}: a 2-D tensor of {' or '.join(str(d) for d in codes)} is needed, "
                          f"got {tuple(t.shape)} {t.dtype}")
     r, c = t.shape
+    if r > _MAX_INT or (c > _MAX_INT and not wide):
+        raise ValueError(f"{name}: shape {(r, c)}, more than 2^31 - 1 rows or columns")
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{name}: shape {(r, c)} where {(rows or r, cols or c)} is needed")
     sr, sc = t.stride()
@@ -574,10 +582,12 @@ def token_logprobs(logits, V: int, temperature: float, targets=None, logp=None, 
     computed. Returns the status tensor."""
     torch = _torch or _import_torch()
     f32, i32 = torch.float32, torch.int32
-    rows, cols, px, ld, code = _rows_of(logits, "logits", _FLOATS)
-    if V > cols:
-        raise ValueError(f"V = {V} above the {cols} columns of logits")
+    rows, cols, px, ld, code = _rows_of(logits, "logits", _FLOATS, wide=True)
+    if V > cols or not -_MAX_INT <= V <= _MAX_INT:
+        raise ValueError(f"V = {V} above the {cols} columns of logits or 2^31 - 1")
     k = 0 if top_ids is None else top_ids.shape[-1]
+    if k > _MAX_INT:
+        raise ValueError(f"top_ids: {k} alternatives, more than 2^31 - 1")
     pt, pl = _vector_of(targets, "targets", i32, rows), _vector_of(logp, "logp", f32, rows)
     pe, ps = _vector_of(entropy, "entropy", f32, rows), _vector_of(lse, "lse", f32, rows)
     pi, pp = _vector_of(top_ids, "top_ids", i32, rows * k), _vector_of(top_logp, "top_logp", f32, rows * k)
@@ -599,10 +609,10 @@ def token_logprobs_bwd(logits, V: int, temperature: float, lse, dlogits, targets
     dlogp and dentropy (rows,) float32 and the forward's lse and entropy. Returns the status tensor."""
     torch = _torch or _import_torch()
     f32 = torch.float32
-    rows, cols, px, ld, code = _rows_of(logits, "logits", _FLOATS)
-    _, dcols, pd, ldd, dcode = _rows_of(dlogits, "dlogits", _FLOATS, rows)
-    if V > cols or V > dcols:
-        raise ValueError(f"V = {V} above the columns of logits or dlogits")
+    rows, cols, px, ld, code = _rows_of(logits, "logits", _FLOATS, wide=True)
+    _, dcols, pd, ldd, dcode = _rows_of(dlogits, "dlogits", _FLOATS, rows, wide=True)
+    if V > cols or V > dcols or not -_MAX_INT <= V <= _MAX_INT:
+        raise ValueError(f"V = {V} above the columns of logits or dlogits, or 2^31 - 1")
     if dcode != code:
         raise ValueError("dlogits: the type of logits is needed")
     pt, pl = _vector_of(targets, "targets", torch.int32, rows), _vector_of(lse, "lse", f32, rows)

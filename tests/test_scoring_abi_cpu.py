@@ -140,3 +140,33 @@ def test_temperatures_past_the_limit_are_refused():
             args = list(ok)
             args[5] = tau
             assert fn(*args) == -1 and said in lib.gpt2_last_error(), (tau, lib.gpt2_last_error())
+
+
+def test_binding_refuses_extents_that_32_bits_would_cut_off():
+    """Sizes go to the library as 32-bit integers: 2^32 + 8 columns must not arrive as 8."""
+    torch = pytest.importorskip("torch")
+    big = (1 << 32) + 8
+
+    def wide(rows, cols, dtype=torch.float32):
+        return torch.empty(1, dtype=dtype).expand(rows, cols) if cols == 1 else torch.empty(
+            (rows, cols), dtype=dtype, device="meta")
+
+    s = torch.zeros(4)
+    for x, q in ((wide(4, big), wide(4, big, torch.int8)), (wide(big, 8), wide(big, 8, torch.int8))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            native.quantize_rows(x, q, s)
+    q = torch.zeros((4, 8), dtype=torch.int8)
+    with pytest.raises(ValueError, match="2\\^31"):
+        native.matmul_i8(q, s, wide(big, 8, torch.int8), s, wide(4, big))
+    with pytest.raises(ValueError, match="2\\^31"):
+        native.matmul_i8(wide(4, big, torch.int8), s, wide(4, big, torch.int8), s, torch.zeros((4, 4)))
+    # logits may have more columns than V; V itself, negative ones among them, is checked
+    for V in (big, -(1 << 32) + 8):
+        with pytest.raises(ValueError, match="V = "):
+            native.token_logprobs(wide(4, 2 * big), V, 1.0, lse=s)
+        with pytest.raises(ValueError, match="V = "):
+            native.token_logprobs_bwd(wide(4, 2 * big), V, 1.0, s, wide(4, 2 * big), entropy=s, dentropy=s)
+    with pytest.raises(ValueError, match="2\\^31"):
+        native.token_logprobs(wide(big, 8), 8, 1.0, lse=wide(1, big)[0])
+    with pytest.raises(ValueError, match="top_ids"):
+        native.token_logprobs(wide(1, 8), 8, 1.0, top_ids=wide(1, big, torch.int32), top_logp=wide(1, big))
