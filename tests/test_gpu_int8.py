@@ -380,3 +380,12 @@ def test_stride_of_a_single_row_does_not_matter():
         np.testing.assert_array_equal(room[:, :K_].cpu().numpy(), want_q)
         np.testing.assert_array_equal(scale.cpu().numpy(), want_s)
         assert torch.all(room[:, K_:] == 77)
+
+
+@pytest.mark.parametrize("M,N,K", [(2500, 4001, 99), (2500, 4001, 257), (1900, 2561, 300), (1700, 3003, 385), (129, 20011, 515)])
+@pytest.mark.parametrize("epilogue,out_dtype", [("bias", torch.bfloat16), ("bias_resid", torch.float32)])
+@pytest.mark.parametrize("shift", [(0, 0, 0), (1, 3, 1)])
+def test_rows_that_start_anywhere_over_several_tiles_a_block(M, N, K, epilogue, out_dtype, shift):
+    """Packed operands, more tiles of 128 x 128 than SMs (up to 640): the ring and both accumulators are used again; one
+    K block, odd and even numbers of them."""
+    _product(M, N, K, epilogue, out_dtype, shift=shift)
