@@ -247,6 +247,9 @@ struct ForwardSmem {
     static_assert(ROOM >= NT / 32 * LOGPROB_MAX_TOP, "each warp's list fits");
     u64 cand[ROOM];                       // keys that reach the bound
     Sums sums[NT / 32];
+    float2 own[NT];                       // the threads' maxima and sums, see sum_without_largest
+    float without[NT / 32];
+    int holder;
     int again[GROUPS];                    // the groups whose values are read again
     int scan[NT / 32];
     unsigned bound;
@@ -256,6 +259,7 @@ struct ForwardSmem {
 // Of a cluster's first block: every block's results.
 struct ClusterSmem {
     Sums sums[8];
+    float without[8];
     u64 top[8 * LOGPROB_MAX_TOP];
 };
 
@@ -504,6 +508,45 @@ struct Part {
     }
 };
 
+// Where the largest token has nearly all of the probability, log s = log(1 + r) with the sum r of all others is small, and
+// s, rounded next to 1, holds little of r: with r = 4e-3 that token's log-probability was off by 1.6e-5 of its value. Up to
+// this s, r is summed by itself; past it log s is above 0.06, and a few 2^-24 of s are some 1e-6 of it. (8192 x 50257 bf16
+// with every row sure: 134 us instead of 128; 20000 x 512: 14.7 instead of 13.)
+constexpr float SURE = 1.0625f;
+__device__ __forceinline__ bool is_sure(float s) { return s >= 1.f && s < SURE; }   // (0: nothing was seen; NaN)
+
+template <int NT>
+__device__ __forceinline__ float sum_of(const float (&v)[NT / 32]) {   // of the warps' values
+    float sum = v[0];
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) sum += v[w];
+    return sum;
+}
+
+// Leaves in sm.without, a warp's part each, the sum of the vectors begin .. end - 1 without the (only) value m that is the
+// largest. The threads' sums are at hand; that of the thread that holds m is made anew from its vectors, by all threads,
+// element by element (a few each, from L2).
+template <typename T, int NT>
+__device__ __forceinline__ void sum_without_largest(ForwardSmem<NT>& sm, const T* x, const RowVecs<T>& rv, int begin, int end,
+                                                    float m, float c) {
+    constexpr int N = RowVecs<T>::N;
+    const int tid = threadIdx.x % NT;
+    const float2 own = sm.own[tid];
+    const bool holds = own.x == m && own.y > 0.f;
+    if (holds) sm.holder = tid;
+    meet<NT>();
+    float sum = holds ? 0.f : own.y * ex2_approx((own.x - m) * c);
+#pragma unroll 1
+    for (int i = begin + sm.holder + tid / N * NT; i < end; i += NT / N * NT) {
+        const int e = rv.first(i) + tid % N;
+        const float d = (e < rv.last(i) ? to_f(x[e]) : NEG_INF) - m;
+        if (d < 0.f) sum += ex2_approx(d * c);
+    }
+    sum = warp_sum(sum);
+    if ((tid & 31) == 0) sm.without[tid >> 5] = sum;
+    meet<NT>();
+}
+
 // Threads of a block: rows of a warp share one.
 template <int NT>
 constexpr int BLOCK_OF = NT < 128 ? 128 : NT;
@@ -592,6 +635,7 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
     }
     // the maximum of all first, so that every thread rescales once
     {
+        sm.own[tid] = make_float2(a.m, a.s);
         float m = warp_max(a.m);
         if (NT > 32) {
             if (lane == 0) sm.sums[tid >> 5].m = m;
@@ -620,15 +664,24 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
             __syncwarp();
         }
     }
+    // (Its place matters to the registers of all rows: after the search, 4096 x 50257 fp32 take 126 us instead of 123 on 256
+    // threads; before it, 8192 x 50257 bf16 130 us instead of 128.5 on 128.)
+    constexpr bool EARLY = sizeof(T) == 4 || NT == 256;
+    if (EARLY && is_sure(a.s)) sum_without_largest<T, NT>(sm, x, rv, begin, end, a.m, c);
     if (out.top_k && (CLUSTER || a.s != 0.f)) Part<T, NT>{sm, x, rv, begin, end}.find_top(out.top_k, a.s != a.s);
+    if (!EARLY && is_sure(a.s)) sum_without_largest<T, NT>(sm, x, rv, begin, end, a.m, c);
     const u64* keys = sm.cand;
     int n_keys = out.top_k ? sm.n_cand : 0;
+    float without = 0.f;
     if constexpr (CLUSTER) {
         __shared__ ClusterSmem cs;
         auto cluster = cg::this_cluster();
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // every block has started
         ClusterSmem* first = cluster.map_shared_rank(&cs, 0);
-        if (tid == 0) first->sums[part] = a;
+        if (tid == 0) {
+            first->sums[part] = a;
+            if (is_sure(a.s)) first->without[part] = sum_of<NT>(sm.without);
+        }
         if (out.top_k) {
             if (tid < out.top_k && tid >= n_keys) first->top[part * out.top_k + tid] = 0;
             for_top(sm.cand, n_keys, out.top_k, NT, [&](int r, u64 k) { first->top[part * out.top_k + r] = k; });
@@ -639,11 +692,20 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
         for (int i = 1; i < parts; ++i) a.join(cs.sums[i], c);
         keys = cs.top;
         n_keys = parts * out.top_k;
+        if (is_sure(a.s)) {   // then the part with the largest value was
+            without = 0.f;
+            for (int i = 0; i < parts; ++i) {
+                const Sums b = cs.sums[i];
+                without += b.m == a.m && b.s > 0.f ? cs.without[i] : b.s * ex2_approx((b.m - a.m) * c);
+            }
+        }
+    } else if (is_sure(a.s)) {
+        without = sum_of<NT>(sm.without);
     }
     griddep_launch();   // the next kernel's blocks may come: not earlier, they would crowd on the SMs with room
     const float z_max = a.m * inv_tau;
     const bool bad = a.s != a.s || z_max == -NEG_INF, empty = !bad && (a.s == 0.f || z_max == NEG_INF);
-    const float log_s = logf(a.s);
+    const float log_s = is_sure(a.s) ? log1pf(without) : logf(a.s);
     auto settle = [&](float v, float nothing) { return bad ? nan_value() : empty ? nothing : v; };
     auto logp_of = [&](float v) {   // (the difference of two logits may pass fp32's range where that of their z does not)
         const float d = v - a.m;

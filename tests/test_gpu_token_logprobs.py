@@ -644,3 +644,47 @@ def test_a_token_further_below_the_largest_than_fp32_reaches(dtype, R, V):
         _close(logp.cpu().numpy(), np.full(R, gap), 6 * EPS * size[0, 1], "logp")
         _close(lse.cpu().numpy(), np.full(R, high / tau), 6 * EPS * high / tau, "lse")
         assert torch.all(H == 0) and ids[0].tolist() == [7] + [v for v in range(20) if v != 7] + [20, 21]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tau", [1.0, 0.7])
+@pytest.mark.parametrize("R,V", [(12, 3), (12, 40), (12, 2000), (1200, 5003), (48, 5003), (12, 50257), (156, 16384), (156, 70001)])
+def test_log_probability_of_a_sure_token(dtype, tau, R, V):
+    """A token that has nearly all of the probability: with r the sum of all others over it, its log-probability is
+    -log(1 + r), near -r, and right relative to that, however small r is; and so is the entropy, log(1 + r) + sum of the
+    others' (m - z) / (1 + r), two numbers of one sign. Relative errors, eps = 2^-24: a term of r has 4 eps of its exponent
+    (d = x - m, 1 / tau, log2(e) / tau, their product), exp's 2^-21; the additions, all of one sign, an eps each (a warp
+    sums V / 64 in a row, 128 and 256 threads fewer), the joins 16; the logarithm and the last operations 6."""
+    from decoder_only_transformer_sm_b200 import native
+    rng = np.random.default_rng(V + R)
+    x = rng.standard_normal((12, V)).astype(np.float32)
+    want_r = np.array([0.3, 0.07, 0.0626, 0.0624, 0.05, 4e-3, 1e-3, 1e-4, 1e-5, 1e-6, 1e-8, 1e-12])
+    at = rng.integers(0, V, 12)
+    at[:3] = 0, V - 1, V // 2
+    others = np.arange(V)[None, :] != at[:, None]
+    x[::3] = np.where(others[::3] & (np.arange(V) % 2 == 1), -np.inf, x[::3])       # masked tokens among the others
+    x = torch.from_numpy(x).to(dtype).float().numpy().astype(np.float64)
+    z0 = np.where(others, x / tau, -np.inf)
+    mass = np.log(np.exp(z0).sum(1)) if V > 3 else np.log(np.maximum(np.exp(z0).sum(1), 1e-3))
+    x[np.arange(12), at] = tau * (mass - np.log(want_r))
+    t = torch.from_numpy(x.astype(np.float32)).to(dtype)
+    x = t.double().numpy()
+    m = x[np.arange(12), at][:, None]
+    d = np.where(others, (x - m) / tau, -np.inf)
+    e = np.exp(d)
+    r = e.sum(1)
+    logp, H = -np.log1p(r), np.log1p(r) - np.where(e > 0, e * np.where(e > 0, d, 0.0), 0.0).sum(1) / (1 + r)
+    far = np.where(e > e.max(1, keepdims=True) * 1e-12, np.abs(np.where(e > 0, d, 0.0)), 0.0).max(1)
+    adds = V / 64 if V <= 2048 or (V <= 8192 and R > 1184) else V / 256
+    rel = 4 * EPS * far + 2.0 ** -21 + (adds + 16 + 6) * EPS
+    rel = np.where(r > 0.0625, rel + (adds + 22) * EPS * 1.1 / np.log1p(r), rel)    # s itself is summed there
+    n = R // 12
+    lp, ent, lse = (torch.empty(R, device="cuda") for _ in range(3))
+    ids, top = torch.empty((R, 2), dtype=torch.int32, device="cuda"), torch.empty((R, 2), device="cuda")
+    targets = torch.from_numpy(np.tile(at, n).astype(np.int32)).cuda()
+    _, dx = _place(t.repeat(n, 1), -V % 8, 0)
+    native.token_logprobs(dx, V, tau, targets=targets, logp=lp, entropy=ent, lse=lse, top_ids=ids, top_logp=top)
+    assert np.array_equal(ids[:, 0].cpu().numpy(), np.tile(at, n))
+    assert torch.equal(top[:, 0], lp)
+    _close(lp.cpu().numpy(), np.tile(logp, n), np.tile(rel * np.abs(logp), n), "logp")
+    _close(ent.cpu().numpy(), np.tile(H, n), np.tile(rel * H + 6 * EPS * H, n), "entropy")
