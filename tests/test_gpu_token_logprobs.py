@@ -688,3 +688,45 @@ def test_log_probability_of_a_sure_token(dtype, tau, R, V):
     assert torch.equal(top[:, 0], lp)
     _close(lp.cpu().numpy(), np.tile(logp, n), np.tile(rel * np.abs(logp), n), "logp")
     _close(ent.cpu().numpy(), np.tile(H, n), np.tile(rel * H + 6 * EPS * H, n), "entropy")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tau", [1.0, 0.7])
+@pytest.mark.parametrize("R,V", [(12, 3), (12, 40), (300, 1000), (12, 5003), (240, 2123), (12, 50257)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_gradient_of_a_sure_target(dtype, tau, R, V, in_place):
+    """1 - p of a target with nearly all of the probability, relative to itself: g (1 - p) = -g expm1(d) with
+    d = (x - tau lse) / tau, where the subtraction rounds once (fma): 3 eps of d, expm1's 2^-22, products 3 eps; the
+    entropy's part h p (d + H) as in the other gradient tests, its p 2^-21 and 4 eps of d off."""
+    from decoder_only_transformer_sm_b200 import native
+    rng = np.random.default_rng(V + R)
+    want_r = np.array([0.3, 0.07, 0.05, 0.02, 4e-3, 1e-3, 1e-4, 3e-5])
+    at = rng.integers(0, V, R)
+    at[:3] = 0, V - 1, V // 2
+    x = rng.standard_normal((R, V))
+    others = np.arange(V)[None, :] != at[:, None]
+    mass = np.log(np.where(others, np.exp(x / tau), 0.0).sum(1))
+    x[np.arange(R), at] = tau * (mass - np.log(want_r[np.arange(R) % 8]))
+    t = torch.from_numpy(x.astype(np.float32)).to(dtype)
+    x = t.double().numpy()
+    z = x / tau
+    lse = np.log(np.exp(z - z.max(1, keepdims=True)).sum(1)) + z.max(1)
+    p = np.exp(z - lse[:, None])
+    H = (-np.where(p > 0, p * (z - lse[:, None]), 0.0).sum(1)).astype(np.float32)
+    lse = lse.astype(np.float32)
+    g = (rng.standard_normal(R) + 2.0).astype(np.float32)
+    h = (rng.standard_normal(R) * (np.arange(R) % 3 == 0)).astype(np.float32)
+    _, dx = _place(t, -V % 8, 0)
+    out = dx if in_place else torch.empty_like(dx)
+    cu = lambda v: torch.from_numpy(v).cuda()  # noqa: E731
+    native.token_logprobs_bwd(dx, V, tau, cu(lse), out, targets=cu(at.astype(np.int32)), dlogp=cu(g), entropy=cu(H),
+                              dentropy=cu(h))
+    got = out[:, :V].double().cpu().numpy()[np.arange(R), at]
+    tau32 = float(np.float32(tau))
+    d = (x[np.arange(R), at] - tau32 * lse.astype(np.float64)) / tau32
+    G, Hd, hd = g.astype(np.float64), H.astype(np.float64), h.astype(np.float64)
+    want = (-G * np.expm1(d) - hd * np.exp(d) * (d + Hd)) / tau32
+    tol = np.abs(G * np.expm1(d)) * (6 * EPS + 2.0 ** -22)
+    tol = tol + np.abs(hd) * ((2.0 ** -21 + 4 * EPS * np.abs(d)) * np.abs(d + Hd) + 6 * EPS * (np.abs(d) + np.abs(Hd)))
+    tol = tol / tau32 + (2.0 ** -8 * 1.01 if dtype == torch.bfloat16 else 2 * EPS) * np.abs(want)
+    _close(got, want, tol, "dlogits of the target")
