@@ -523,7 +523,10 @@ def _device_of(first, *rest):
 
 def _status_on(dev, stream):
     """A cleared status word, made on the stream that the kernel will run on."""
-    on = _torch.cuda.ExternalStream(stream, device=dev) if stream else _torch.cuda.default_stream(dev)
+    if isinstance(stream, _torch.cuda.Stream):   # ctypes takes its handle from it
+        on = stream
+    else:
+        on = _torch.cuda.ExternalStream(stream, device=dev) if stream else _torch.cuda.default_stream(dev)
     with _torch.cuda.device(dev), _torch.cuda.stream(on):
         return _torch.zeros(1, dtype=_torch.int32, device=dev)
 

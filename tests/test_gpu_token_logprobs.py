@@ -730,3 +730,24 @@ def test_gradient_of_a_sure_target(dtype, tau, R, V, in_place):
     tol = tol + np.abs(hd) * ((2.0 ** -21 + 4 * EPS * np.abs(d)) * np.abs(d + Hd) + 6 * EPS * (np.abs(d) + np.abs(Hd)))
     tol = tol / tau32 + (2.0 ** -8 * 1.01 if dtype == torch.bfloat16 else 2 * EPS) * np.abs(want)
     _close(got, want, tol, "dlogits of the target")
+
+
+def test_stream_given_as_a_handle_or_as_a_torch_stream():
+    """With and without a status tensor, as the other bindings of the library take it."""
+    from decoder_only_transformer_sm_b200 import native
+    x = torch.randn((3, 500), generator=torch.Generator().manual_seed(0)).cuda()
+    want = torch.empty(3, device="cuda")
+    native.token_logprobs(x, 500, 1.0, lse=want)
+    q, s = torch.empty((3, 500), dtype=torch.int8, device="cuda"), torch.empty(3, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream, torch.cuda.default_stream(), 0):
+        for status in (None, torch.zeros(1, dtype=torch.int32, device="cuda")):
+            torch.cuda.synchronize()
+            lse, d, out = torch.empty(3, device="cuda"), torch.empty_like(x), torch.empty((3, 3), device="cuda")
+            native.quantize_rows(x, q, s, stream=stream)
+            got = [native.token_logprobs(x, 500, 1.0, lse=lse, status=status, stream=stream),
+                   native.token_logprobs_bwd(x, 500, 1.0, lse, d, entropy=lse, dentropy=lse, status=status, stream=stream),
+                   native.matmul_i8(q, s, q, s, out, status=status, stream=stream)]
+            torch.cuda.synchronize()
+            assert torch.equal(lse, want) and all(int(v.item()) == 0 for v in got)
