@@ -6,7 +6,10 @@
 // rounded once to fp32 and multiplied by sa[m], then sb[n], in fp32.
 //
 // Chosen by the shape and the alignment of the operands:
-//   M <= 8                 weight streaming (k_matmul_i8_rows.cu): bound by reading B once
+//   M <= 8                 weight streaming (k_matmul_i8_rows.cu): bound by reading B once. The tensor cores have a tile's
+//                          start and chain of K blocks whatever M: 8 x 2304 x 768 2.8 us streamed, 5.5 with them, 8 x 6400
+//                          x 1600 7.7 (weights from memory) and 10.6; only a vocabulary's width evens that out (x 50304 x
+//                          768, weights from memory: M = 4 13.3 and 16.7, 5 16.6 and 14.1, 8 17.6 and 15.6)
 //   M > 8, 16-byte rows    tcgen05 (kind::i8) with TMA operands
 //   M > 8, other rows      tcgen05 with operands that warps put together from aligned words
 #include <cudaTypedefs.h>
@@ -45,8 +48,10 @@ __device__ __forceinline__ f32x2 finish2(int a0, int a1, f32x2 sa, f32x2 sb, f32
 }
 
 // ---------------------------------------------------------------- tensor cores
-// 16384 x 2304 x 768 with bias 31 us (1.9 POP/s; writing the 75 MB result alone takes 22.6 us), 16384 x 768 x 768 with
-// residual 29 us, 2048 x 6400 x 1600 with GELU 26 us, 8192^3 400 us (2.7 POP/s; 330 us with operands of zeros: power).
+// From a CUDA graph, three sets of operands in turn: 16384 x 2304 x 768 with bias 30 us (1.9 POP/s), 16384 x 768 x 768 with
+// residual 29 us, 2048 x 6400 x 1600 with GELU 25 us; in long runs, under the power cap, the first takes 36.5 us (1.6 POP/s),
+// the last 28. 8192^3 400 us (2.7 POP/s; 330 us with operands of zeros: power). With bf16 results the epilogue is the longer
+// part of a tile up to some ten K blocks: 16384 x 2304 takes 18 us with one, 30 with six, 92 with 25 (3.1 a block and 14).
 //
 // Persistent kernel: a CTA, or a pair of CTAs (a cluster of two, cta_group::2), walks output
 // tiles of 128 CTAS x BN. Warp 0 streams 128-byte-wide K blocks of both operands with TMA into a
@@ -612,7 +617,8 @@ bool launch_tc(const Ctx& ctx, const I8Product& p) {
         !make_map(&tb, I8, 1, p.B, p.N, p.K, p.ldb, L::BK, L::B_ROWS)))
         return false;
     // TMA stores are asynchronous, but their bursts hold up the operands' loads: they pay for fp32 results
-    // and short sums (16384 x 2304 in bf16: K = 128 21 us against 27 with plain stores, K = 768 35.6 against 33.4).
+    // and short sums (16384 x 2304 in bf16: K = 128 19.2 us against 22.2 with plain stores, K = 768 31.7 against 30.4;
+    // 16384 x 768 x 768 in fp32 with residual 28.7 against 31.1).
     // They write whole 16-byte segments, so a row that ends inside one (its padding is the caller's) is not theirs.
     g.tma_out = g.vec_out && (p.N * sizeof(O)) % 16 == 0 && (sizeof(O) == 4 || g.k_blocks <= 4);
     if (g.tma_out) {

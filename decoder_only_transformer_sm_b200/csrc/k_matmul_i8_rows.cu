@@ -4,8 +4,8 @@
 // L1. Lane r * MM + m finishes element (m, n0 + r); its scales are requested first, so that a
 // warp's life is about one trip to memory.
 //
-// lm_head of one token (50304 x 768): 4.6 us with the weights in L2, 7.4 us from memory (5.3 TB/s),
-// of which about 2 us are the launch and the first load; 8 rows 12.6 and 17.8 us, where the loads
+// lm_head of one token (50304 x 768, from a CUDA graph): 6.6 us with the weights in L2, 7.3 us from memory (5.3 TB/s),
+// of which about 2 us are the launch and the first load; 2 rows 6.9 and 11 us, 8 rows 13.2 and 17.6 us, where the loads
 // of the rows of A from L1 are as many as those of B.
 #include "kernels.cuh"
 

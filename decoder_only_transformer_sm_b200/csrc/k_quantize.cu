@@ -22,7 +22,9 @@
 // and after its last one are held one a thread, and the codes go through shared memory,
 // laid out there like the memory they go to, so that they leave in 16-byte stores too. Where
 // rows and codes are whole vectors (ALIGNED) none of that is needed: the codes go straight out.
-// 50257 x 1024 fp32 38 us (6.8 TB/s), 4096 x 6400 bf16 15 us (5.1 TB/s), 16384 x 1599 bf16 22.6 us.
+// 50257 x 1024 fp32 38 us (6.8 TB/s), 4096 x 6400 bf16 13.4 us (5.9 TB/s), 16384 x 1599 bf16 21.3 us, 16384 x 1600 14.2 (from
+// a CUDA graph on the same buffers). Rows that do not fit in registers (past 8192 fp32 or 16384 bf16 values) are read twice,
+// value by value: 4096 x 8200 fp32 45.7 us, 4096 x 8192 25.7; 2048 x 16400 bf16 50.3, 2048 x 16384 17.4.
 #include "kernels.cuh"
 
 namespace gpt2 {

@@ -21,7 +21,8 @@
 // row's order after them; the same way -inf fills up where fewer than top_k threads saw a number.
 // (Where even the larger ones are too many, a few threads holding most of a row's largest values,
 // each warp keeps a sorted list.)
-// 8192 x 50257 bf16: 135 us without alternatives (6.1 TB/s), 153 with five, 229 with 32.
+// 8192 x 50257 bf16: 129 us without alternatives (6.4 TB/s), 150 with five, 231 with 32 (normal logits, from a CUDA graph,
+// two sets of them in turn; with a favoured token in each row, as a model's, 170 with five).
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -857,17 +858,17 @@ void launch_token_logprobs(const Ctx& ctx, const T* logits, long long ld, int ro
                            const int* targets, const LogprobOut& out) {
     const float inv_tau = 1.f / temperature;
     // A warp a row where the row is short, and with many rows up to 8192: no block to wait for (8192 rows of 1024 bf16
-    // logits 11.8 us against 22, of 8192 with five alternatives 40.7 against 50.8). For many alternatives, which a warp
-    // takes longer to rank, only with many rows, of up to 16 KB (with 20: 20000 x 512 bf16 38 us against 92, 8192 x
-    // 8192 53 against 65; but 8192 x 6000 fp32 61 against 56, 200 x 1500 6.6 against 4.9).
+    // logits 9.1 us against 18.4, of 8192 with five alternatives 38.5 against 41.7). For many alternatives, which a warp
+    // takes longer to rank, only with many rows, of up to 16 KB (with 20: 20000 x 512 bf16 39 us against 90, 8192 x
+    // 8192 54 against 63; but 8192 x 6000 fp32 61.6 against 56.8, 200 x 1500 7.0 against 5.6).
     const bool many = rows >= 8 * ctx.num_sms;
     const bool warp = out.top_k <= WALK ? V <= 2048 || (V <= 8192 && many) : many && V <= 16384 / (int)sizeof(T);
     // Few rows: as many blocks a row as give every SM two, while a thread still has a vector.
     int parts = 8;
     while (parts > 1 && ((long long)rows * parts > 2 * ctx.num_sms || V < parts * 128 * RowVecs<T>::N)) parts /= 2;
     // 256 threads for rows of 120 KB and more: with 128, the rows under way together are more than L2 holds, and what
-    // is read again comes from memory (4096 x 131072 bf16, five alternatives: 193 us against 254; 8192 x 16384: 79
-    // against 60).
+    // is read again comes from memory (4096 x 131072 bf16, five alternatives: 179 us against 202; 4096 x 50257 fp32
+    // 136 against 152; but 8192 x 16384 bf16 80 against 58).
     if (warp) launch_rows<T, 32>(ctx, logits, ld, rows, V, inv_tau, targets, out);
     else if (parts > 1) launch_split<T>(ctx, logits, ld, rows, V, inv_tau, targets, out, parts);
     else if (V >= 120000 / (int)sizeof(T)) launch_rows<T, 256>(ctx, logits, ld, rows, V, inv_tau, targets, out);
@@ -880,8 +881,8 @@ void launch_token_logprobs_bwd(const Ctx& ctx, const T* logits, long long ld, in
                                const int* targets, const float* lse, const float* dlogp, const float* entropy,
                                const float* dentropy, T* dlogits, long long ldd) {
     // As few threads a row, 32 at least and 256 at most, as leave a thread four vectors or one round of loads. With 256
-    // for every row 12149 x 2123 bf16 take 63 us instead of 32, 20000 x 1000 63 instead of 18, 64 x 1000 2.1 instead of 2.5;
-    // with one row a block 100000 x 65 fp32 take 105 us instead of 43.
+    // for every row 12149 x 2123 bf16 take 57 us instead of 29, 20000 x 1000 60 instead of 17, 64 x 1000 2.5 instead of 2.9;
+    // with one row a block 100000 x 65 fp32 take 104 us instead of 44.5.
     const int vecs = V / RowVecs<T>::N + 2;
     auto launch = [&](auto threads) {
         constexpr int NT = decltype(threads)::value, ROWS = NT < 128 ? 128 / NT : 1;

@@ -186,7 +186,8 @@ int gpt2k_embedding_bwd_workspace(int B, int T, int C, int64_t* floats);
  * q is int8 in [-127, 127], row stride ldq bytes; bytes K .. ldq - 1 of a row are
  * left as they are. A row of zeros has scale 0 and codes 0; a row with a NaN or
  * an infinity has scale NaN and codes 0, so that its products are NaN. x and q
- * may start anywhere an element may; 16-byte aligned rows are fastest. Errors:
+ * may start anywhere an element may; 16-byte aligned rows are fastest, and rows
+ * past 8192 fp32 or 16384 bf16 values take two to four times as long. Errors:
  * INVALID_ARG (unknown dtype, rows or K < 1 or above 2^30, a stride below K, a
  * NULL or misaligned pointer). */
 int gpt2k_quantize_rows(int dtype, const void* x, int rows, int K, int64_t ldx, int8_t* q, int64_t ldq,
@@ -206,10 +207,11 @@ int gpt2k_quantize_rows(int dtype, const void* x, int rows, int K, int64_t ldx, 
  * out has row stride ldo elements; columns N .. ldo - 1 are left as they are.
  * out must not overlap A or B. Operands may start anywhere an element may:
  * A and B whose first byte and row stride are multiples of 16 are loaded by
- * TMA or, for a few rows, streamed; other ones are put together from bytes
- * (slower). Errors: INVALID_ARG (sizes < 1, M or N above 2^30, K > 131071, a
- * stride below its row, another epilogue, an operand of the epilogue missing, bias_resid with a bf16
- * result or in place with another stride, a NULL or misaligned pointer). */
+ * TMA or, for a few rows, streamed; other ones are put together from aligned
+ * 32-bit words (slower; a single row's stride does not matter). Errors:
+ * INVALID_ARG (sizes < 1, M or N above 2^30, K > 131071, a stride below its
+ * row, another epilogue, an operand of the epilogue missing, bias_resid with a
+ * bf16 result or in place with another stride, a NULL or misaligned pointer). */
 int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scale, const int8_t* B, int64_t ldb,
                     const float* b_scale, int M, int N, int K, int epilogue, int out_dtype, void* out, int64_t ldo,
                     const float* bias, const float* resid, int64_t ldr, uint32_t* status_dev, void* stream);
@@ -220,7 +222,8 @@ int gpt2k_matmul_i8(const int8_t* A, int64_t lda, const float* a_scale, const in
  * z = logits / temperature in fp32 (past fp32's range: an infinity), p =
  * softmax(z). A z of -inf is a masked token.
  *   lse[r]     = log sum_v exp(z_v)
- *   logp[r]    = z[targets[r]] - lse[r]; 0 where targets[r] is -1
+ *   logp[r]    = z[targets[r]] - lse[r]; 0 where targets[r] is -1 (not from the
+ *                rounded lse: right relative to itself also for a sure token)
  *   entropy[r] = -sum_v p_v log p_v  (nats; masked tokens add 0)
  *   top_ids, top_logp (rows, top_k): the top_k largest logits' indices and log
  *                probabilities, largest first, equal values by lowest index
