@@ -185,11 +185,11 @@ int gpt2k_embedding_bwd_workspace(int B, int T, int C, int64_t* floats);
  *              even (of the exact quotient: the codes depend on no rounding).
  * q is int8 in [-127, 127], row stride ldq bytes; bytes K .. ldq - 1 of a row are
  * left as they are. A row of zeros has scale 0 and codes 0; a row with a NaN or
- * an infinity has scale NaN and codes 0, so that its products are NaN. x and q
- * may start anywhere an element may; 16-byte aligned rows are fastest, and rows
- * past 8192 fp32 or 16384 bf16 values take two to four times as long. Errors:
- * INVALID_ARG (unknown dtype, rows or K < 1 or above 2^30, a stride below K, a
- * NULL or misaligned pointer). */
+ * an infinity has scale NaN and codes 0, so that its products are NaN. q and
+ * scale must not overlap x. x and q may start anywhere an element may; 16-byte
+ * aligned rows are fastest, and rows past 8192 fp32 or 16384 bf16 values take
+ * two to four times as long. Errors: INVALID_ARG (unknown dtype, rows or K < 1
+ * or above 2^30, a stride below K, a NULL or misaligned pointer). */
 int gpt2k_quantize_rows(int dtype, const void* x, int rows, int K, int64_t ldx, int8_t* q, int64_t ldq,
                         float* scale, void* stream);
 
