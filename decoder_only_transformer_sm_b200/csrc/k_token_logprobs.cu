@@ -248,7 +248,7 @@ struct ForwardSmem {
     static_assert(ROOM >= NT / 32 * LOGPROB_MAX_TOP, "each warp's list fits");
     u64 cand[ROOM];                       // keys that reach the bound
     Sums sums[NT / 32];
-    float2 own[NT];                       // the threads' maxima and sums, see sum_without_largest
+    float2 own[NT > 32 ? NT : 1];         // the threads' maxima and sums, see sum_without_largest
     float without[NT / 32];
     int holder;
     int again[GROUPS];                    // the groups whose values are read again
@@ -512,9 +512,19 @@ struct Part {
 // Where the largest token has nearly all of the probability, log s = log(1 + r) with the sum r of all others is small, and
 // s, rounded next to 1, holds little of r: with r = 4e-3 that token's log-probability was off by 1.6e-5 of its value. Up to
 // this s, r is summed by itself; past it log s is above 0.06, and a few 2^-24 of s are some 1e-6 of it. (8192 x 50257 bf16
-// with every row sure: 134 us instead of 128; 20000 x 512: 14.7 instead of 13.)
+// with every row sure: 134 us instead of 128; 20000 x 512: 14.3 instead of 13.)
 constexpr float SURE = 1.0625f;
 __device__ __forceinline__ bool is_sure(float s) { return s >= 1.f && s < SURE; }   // (0: nothing was seen; NaN)
+// log(1 + r) for r up to 1/16 by its series, cut off at r^7 / 8 < 5e-10 of it (log1pf costs short rows 1%).
+__device__ __forceinline__ float log_1p_small(float r) {
+    float v = 1.f / 7.f;
+    v = fmaf(-r, v, 1.f / 6.f);
+    v = fmaf(-r, v, 1.f / 5.f);
+    v = fmaf(-r, v, 1.f / 4.f);
+    v = fmaf(-r, v, 1.f / 3.f);
+    v = fmaf(-r, v, 0.5f);
+    return fmaf(-r * r, v, r);
+}
 
 template <int NT>
 __device__ __forceinline__ float sum_of(const float (&v)[NT / 32]) {   // of the warps' values
@@ -524,28 +534,37 @@ __device__ __forceinline__ float sum_of(const float (&v)[NT / 32]) {   // of the
     return sum;
 }
 
-// Leaves in sm.without, a warp's part each, the sum of the vectors begin .. end - 1 without the (only) value m that is the
-// largest. The threads' sums are at hand; that of the thread that holds m is made anew from its vectors, by all threads,
-// element by element (a few each, from L2).
+// The sum of the vectors begin .. end - 1 without the (only) value m that is the largest. The threads' sums are at hand (own,
+// each from the thread's maximum on); that of the thread that holds m is made anew from its vectors, by all threads, element
+// by element (a few each, from L2). A warp's lanes have the result, of a block's warps each leaves its part in sm.without.
 template <typename T, int NT>
-__device__ __forceinline__ void sum_without_largest(ForwardSmem<NT>& sm, const T* x, const RowVecs<T>& rv, int begin, int end,
-                                                    float m, float c) {
+__device__ __forceinline__ float sum_without_largest(ForwardSmem<NT>& sm, const T* x, const RowVecs<T>& rv, int begin, int end,
+                                                     float m, float c, float2 own) {
     constexpr int N = RowVecs<T>::N;
     const int tid = threadIdx.x % NT;
-    const float2 own = sm.own[tid];
+    if (NT > 32) own = sm.own[tid];
     const bool holds = own.x == m && own.y > 0.f;
-    if (holds) sm.holder = tid;
-    meet<NT>();
+    int holder = 0;
+    if (NT > 32) {
+        if (holds) sm.holder = tid;
+        meet<NT>();
+        holder = sm.holder;
+    } else {
+        holder = __ffs(__ballot_sync(0xffffffffu, holds)) - 1;
+    }
     float sum = holds ? 0.f : own.y * ex2_approx((own.x - m) * c);
 #pragma unroll 1
-    for (int i = begin + sm.holder + tid / N * NT; i < end; i += NT / N * NT) {
+    for (int i = begin + holder + tid / N * NT; i < end; i += NT / N * NT) {
         const int e = rv.first(i) + tid % N;
         const float d = (e < rv.last(i) ? to_f(x[e]) : NEG_INF) - m;
         if (d < 0.f) sum += ex2_approx(d * c);
     }
     sum = warp_sum(sum);
-    if ((tid & 31) == 0) sm.without[tid >> 5] = sum;
-    meet<NT>();
+    if (NT > 32) {
+        if ((tid & 31) == 0) sm.without[tid >> 5] = sum;
+        meet<NT>();
+    }
+    return sum;
 }
 
 // Threads of a block: rows of a warp share one.
@@ -635,8 +654,10 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
         }
     }
     // the maximum of all first, so that every thread rescales once
+    const float2 own = make_float2(a.m, a.s);
+    float without = 0.f;
     {
-        sm.own[tid] = make_float2(a.m, a.s);
+        if (NT > 32) sm.own[tid] = own;
         float m = warp_max(a.m);
         if (NT > 32) {
             if (lane == 0) sm.sums[tid >> 5].m = m;
@@ -668,12 +689,11 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
     // (Its place matters to the registers of all rows: after the search, 4096 x 50257 fp32 take 126 us instead of 123 on 256
     // threads; before it, 8192 x 50257 bf16 130 us instead of 128.5 on 128.)
     constexpr bool EARLY = sizeof(T) == 4 || NT == 256;
-    if (EARLY && is_sure(a.s)) sum_without_largest<T, NT>(sm, x, rv, begin, end, a.m, c);
+    if (EARLY && is_sure(a.s)) without = sum_without_largest<T, NT>(sm, x, rv, begin, end, a.m, c, own);
     if (out.top_k && (CLUSTER || a.s != 0.f)) Part<T, NT>{sm, x, rv, begin, end}.find_top(out.top_k, a.s != a.s);
-    if (!EARLY && is_sure(a.s)) sum_without_largest<T, NT>(sm, x, rv, begin, end, a.m, c);
+    if (!EARLY && is_sure(a.s)) without = sum_without_largest<T, NT>(sm, x, rv, begin, end, a.m, c, own);
     const u64* keys = sm.cand;
     int n_keys = out.top_k ? sm.n_cand : 0;
-    float without = 0.f;
     if constexpr (CLUSTER) {
         __shared__ ClusterSmem cs;
         auto cluster = cg::this_cluster();
@@ -700,13 +720,13 @@ __global__ void __launch_bounds__(BLOCK_OF<NT>) token_logprobs_kernel(const T* _
                 without += b.m == a.m && b.s > 0.f ? cs.without[i] : b.s * ex2_approx((b.m - a.m) * c);
             }
         }
-    } else if (is_sure(a.s)) {
+    } else if (NT > 32 && is_sure(a.s)) {
         without = sum_of<NT>(sm.without);
     }
     griddep_launch();   // the next kernel's blocks may come: not earlier, they would crowd on the SMs with room
     const float z_max = a.m * inv_tau;
     const bool bad = a.s != a.s || z_max == -NEG_INF, empty = !bad && (a.s == 0.f || z_max == NEG_INF);
-    const float log_s = is_sure(a.s) ? log1pf(without) : logf(a.s);
+    const float log_s = is_sure(a.s) ? log_1p_small(without) : logf(a.s);
     auto settle = [&](float v, float nothing) { return bad ? nan_value() : empty ? nothing : v; };
     auto logp_of = [&](float v) {   // (the difference of two logits may pass fp32's range where that of their z does not)
         const float d = v - a.m;
